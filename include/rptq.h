@@ -76,6 +76,8 @@ typedef struct CUstream_st *rptq_stream_t;
 #define RPTQ_MAX_CHANNELS 16384
 /* Largest cluster count g. */
 #define RPTQ_MAX_CLUSTERS 512
+/* Most positions a sequence of the paged cache can have room for (max_pages * page_size). */
+#define RPTQ_MAX_POSITIONS (1 << 30)
 
 /* Human-readable text of a status code (static storage, never NULL). */
 const char *rptq_status_string(int status);
@@ -91,6 +93,8 @@ int rptq_version(void);
 #define RPTQ_DEVERR_CLUSTER_ID 1 /* a cluster id was outside [0, g); cluster 0 was used */
 #define RPTQ_DEVERR_REORDER 2    /* an R entry was outside [0, C) */
 #define RPTQ_DEVERR_TIMEOUT 4    /* a bounded wait on an asynchronous copy ran out */
+#define RPTQ_DEVERR_PAGE 8       /* a page id was outside [0, n_pages) */
+#define RPTQ_DEVERR_RANGE 16     /* a sequence's rows, length or positions were out of range */
 int rptq_device_error(rptq_stream_t stream, int *code);
 
 /*
@@ -333,6 +337,109 @@ int rptq_kv_decode_attention(const float *q, int B, int H, int D, const uint8_t 
                              const int32_t *cluster_k, const float *scale_k, const int32_t *zero_k,
                              const int32_t *cluster_v, const float *scale_v, const int32_t *zero_v,
                              int g, int bits, float scale, float *out, rptq_stream_t stream);
+
+/*
+ * The paged packed K/V cache: sequences of unequal length in one pool of pages, for serving.
+ * [RPTQ-art] results paragraph (K/V cache quantized per cluster) and closing memory paragraph (the
+ * cache dominates memory at large batch x sequence).  The four calls below share these arguments:
+ *   k_pages, v_pages  uint8 [n_pages, H, P, D*bits/8], P = page_size: the packed codes of
+ *                rptq_kv_quant, the P slots of one (page, head) contiguous.
+ *   page_table   int32 [B, max_pages]: position p of sequence b lives in page
+ *                page_table[b][p / P], slot p % P.  Entries past a sequence's last page are not read.
+ *   start        int32 [B + 1], non-decreasing: rows start[b] .. start[b+1]-1 of a ragged batch of T
+ *                rows belong to sequence b (none, one or many); rows outside
+ *                [start[0], start[B]) belong to no sequence and are left as they are.
+ *   lens         int32 [B]: positions of each sequence, the rows of this batch counted: with
+ *                n = start[b+1] - start[b], row start[b] + i is position lens[b] - n + i.
+ *   weights      fp32 [n_pages, H, P]: the running sum of attention weights of every position.
+ * The tables are read on the device when the kernels run, so a captured graph follows them.  A
+ * sequence whose tables contradict the call (rows outside [0, T), a length outside
+ * [0, max_len] or, where there is no max_len, [0, max_pages * P]) sets RPTQ_DEVERR_RANGE and is left
+ * out: its outputs stay as they were.  A page id outside [0, n_pages) sets RPTQ_DEVERR_PAGE; what
+ * is then done is said at each call, and nothing outside the pool is touched.
+ * A page that a call writes (append, weights, evict) must belong to one sequence only; pages that
+ * are only read may be shared.
+ * Shapes: D a multiple of 32, 32 <= D <= 256, H*D <= RPTQ_MAX_CHANNELS, P a power of two in
+ * [16, 256], max_pages * P <= RPTQ_MAX_POSITIONS (RPTQ_ERR_UNSUPPORTED otherwise); pools and row
+ * tensors 16-byte aligned, row strides multiples of 16 bytes.  T == 0 or B == 0 is valid: nothing
+ * is launched and no pointer is read.
+ */
+
+/*
+ * New tokens' K and V quantized into their pages: the codes are exactly rptq_kv_quant's.
+ *   k_new, v_new  [T, H, D] of `dtype`, rows row_stride elements apart (the heads of a row
+ *                contiguous); either may be NULL, not both.
+ *   weights      NULL, or the running sums, set to 0 at the written positions (needs k_new).
+ * Positions below 0 (lens[b] < n) and rows whose page id is out of range are not written; every
+ * other byte of the pools is left as it is.
+ */
+int rptq_kv_paged_append(const void *k_new, const void *v_new, int dtype, int64_t T, int H, int D,
+                         int64_t row_stride, const int32_t *start, const int32_t *lens, int B,
+                         const int32_t *page_table, int max_pages, int64_t n_pages, int page_size,
+                         const int32_t *cluster_k, const float *scale_k, const int32_t *zero_k,
+                         const int32_t *cluster_v, const float *scale_v, const int32_t *zero_v, int g,
+                         int bits, uint8_t *k_pages, uint8_t *v_pages, float *weights,
+                         rptq_stream_t stream);
+
+/*
+ * Positions of a paged pool read back as dense values s_k * (q - z_k) (rptq_dequant's).
+ *   pages        k_pages or v_pages, with that tensor's cluster, scale, zero.
+ *   start, begin  row start[b] + i of `out` is position begin[b] + i of sequence b.
+ *   out          [T, H, D] of out_dtype.
+ * Rows whose position or page id is out of range are left as they are.
+ */
+int rptq_kv_paged_dequant(const uint8_t *pages, int H, int D, int bits, const int32_t *start,
+                          const int32_t *begin, int B, const int32_t *page_table, int max_pages,
+                          int64_t n_pages, int page_size, int64_t T, const int32_t *cluster,
+                          const float *scale, const int32_t *zero, int g, void *out, int out_dtype,
+                          rptq_stream_t stream);
+
+/*
+ * Causal softmax attention of each sequence's newest tokens (one at a decode step, a chunk of a
+ * prompt, any mixture) over all its positions, the tokens' own included (append first).  Row
+ * t = start[b] + i, query head a, K/V head h = a / (Hq / H), over positions p <= lens[b] - n + i:
+ *   x_p = scale * sum_d q[t,a,d] K_pd,  w = softmax(x),  out[t,a,d] = sum_p w_p V_pd,
+ *   weights[p] of head h += w_p, summed over the sequence's rows and the head's Hq / H query heads.
+ * A row that sees no position (lens[b] - n + i < 0) gets out = 0.
+ *   q, out       [T, Hq, D] of `dtype`; q's rows q_stride elements apart, out's dense.
+ *   max_q, max_len  bounds on the new rows and the length of any sequence (host values: they size
+ *                the launch; a sequence beyond them is out of range).
+ *   scale        > 0, or 0 for 1 / sqrt(D).
+ *   weights      NULL, or the running sums to add to.
+ *   workspace    rptq_kv_paged_attention_workspace_size(...) bytes (0: may be NULL), 16-byte
+ *                aligned; no initialisation, garbage afterwards.  Calls that may overlap need one each.
+ * Sums, softmax statistics and outputs before their rounding to `dtype` are fp32.  Results do not
+ * change from run to run.  A page id out of range is read as page 0 (no weight is added there).
+ */
+size_t rptq_kv_paged_attention_workspace_size(int64_t T, int Hq, int H, int D, int dtype, int B,
+                                              int max_q, int max_len, int weights);
+int rptq_kv_paged_attention(const void *q, int dtype, int64_t T, int Hq, int H, int D, int64_t q_stride,
+                            const int32_t *start, const int32_t *lens, int B, int max_q, int max_len,
+                            const int32_t *page_table, int max_pages, int64_t n_pages, int page_size,
+                            const uint8_t *k_pages, const uint8_t *v_pages, const int32_t *cluster_k,
+                            const float *scale_k, const int32_t *zero_k, const int32_t *cluster_v,
+                            const float *scale_v, const int32_t *zero_v, int g, int bits, float scale,
+                            void *out, float *weights, void *workspace, size_t workspace_bytes,
+                            rptq_stream_t stream);
+
+/*
+ * Eviction by accumulated attention weight: every (sequence, head) with lens[b] > budget keeps its
+ * last `recent` positions and, of the others, the budget - recent with the largest running sums
+ * (equal sums: the lower positions; NaN counts as the smallest).  The kept positions' codes (K and
+ * V) and sums move, in order, to positions 0 .. budget - 1 of the sequence's own pages; heads of one
+ * sequence may keep different positions.  Everything behind stays as it was; pages past
+ * ceil(new_lens[b] / P) are the caller's again.
+ *   lens         int32 [B], each at most max_len (a host bound, at most max_pages * P).
+ *   new_lens     int32 [B] output: min(lens[b], budget).  Must not overlap lens.
+ *   kept         int32 [B, H, budget] output: the old position of each kept one, ascending; -1 past
+ *                new_lens[b].
+ * 1 <= budget, 0 <= recent <= budget.  A sequence that is out of range, or to be evicted with a page
+ * id out of range, is left as it is: new_lens[b] = lens[b], kept = -1.  B == 0 is valid.
+ */
+int rptq_kv_paged_evict(uint8_t *k_pages, uint8_t *v_pages, float *weights, int B, int H, int D,
+                        int bits, const int32_t *lens, const int32_t *page_table, int max_pages,
+                        int64_t n_pages, int page_size, int max_len, int budget, int recent,
+                        int32_t *new_lens, int32_t *kept, rptq_stream_t stream);
 
 /*
  * Offline weight preparation for the linear layer that reads the reordered activations.

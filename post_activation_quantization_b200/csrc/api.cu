@@ -416,6 +416,139 @@ int rptq_kv_decode_attention(const float *q, int B, int H, int D, const uint8_t 
     return cuda_status(launch_kv_attention(a));
 }
 
+// ---- the paged K/V cache ----------------------------------------------------------------------
+namespace {
+// Sizes of a paged pool; on RPTQ_OK *shift is log2 of the page size.
+int paged_shape(int H, int D, int bits, int B, int max_pages, int64_t n_pages, int page_size, int *shift)
+{
+    if (bits != 3 && bits != 4) return RPTQ_ERR_UNSUPPORTED;
+    if (D < 32 || D > 256 || D % 32 != 0 || H <= 0 || (int64_t)H * D > RPTQ_MAX_CHANNELS) return RPTQ_ERR_UNSUPPORTED;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return RPTQ_ERR_UNSUPPORTED;
+    if (B < 0 || max_pages < 1 || n_pages < 1) return RPTQ_ERR_INVALID_ARG;
+    if ((int64_t)max_pages * page_size > RPTQ_MAX_POSITIONS || n_pages > 0x7fffffffLL) return RPTQ_ERR_UNSUPPORTED;
+    if ((int64_t)B * H > 0x3fffffffLL) return RPTQ_ERR_UNSUPPORTED;
+    *shift = 0;
+    while ((1 << *shift) < page_size) ++*shift;
+    return RPTQ_OK;
+}
+}  // namespace
+
+int rptq_kv_paged_append(const void *k_new, const void *v_new, int dtype, int64_t T, int H, int D,
+                         int64_t row_stride, const int32_t *start, const int32_t *lens, int B,
+                         const int32_t *page_table, int max_pages, int64_t n_pages, int page_size,
+                         const int32_t *cluster_k, const float *scale_k, const int32_t *zero_k,
+                         const int32_t *cluster_v, const float *scale_v, const int32_t *zero_v, int g,
+                         int bits, uint8_t *k_pages, uint8_t *v_pages, float *weights,
+                         rptq_stream_t stream)
+{
+    int shift;
+    if (!dtype_ok(dtype)) return RPTQ_ERR_UNSUPPORTED;
+    if (int st = paged_shape(H, D, bits, B, max_pages, n_pages, page_size, &shift)) return st;
+    if (T < 0 || g <= 0) return RPTQ_ERR_INVALID_ARG;
+    if (row_stride < (int64_t)H * D || row_stride * esize(dtype) % 16 != 0) return RPTQ_ERR_INVALID_ARG;
+    if (T > 0x7fffffffLL) return RPTQ_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0) return RPTQ_OK;
+    if (!start || !lens || !page_table || (!k_new && !v_new)) return RPTQ_ERR_INVALID_ARG;
+    if (k_new && (!cluster_k || !scale_k || !zero_k || !k_pages || !aligned16(k_new) || !aligned16(k_pages)))
+        return RPTQ_ERR_INVALID_ARG;
+    if (v_new && (!cluster_v || !scale_v || !zero_v || !v_pages || !aligned16(v_new) || !aligned16(v_pages)))
+        return RPTQ_ERR_INVALID_ARG;
+    if (weights && !k_new) return RPTQ_ERR_INVALID_ARG;  // the sums belong to the keys' positions
+    DevInfo d;
+    int st = dev_info(&d);
+    if (st) return st;
+    PagedAppendArgs a{k_new, v_new, dtype, T, row_stride, H, D, start, lens, page_table, B, max_pages, shift,
+                      n_pages, max_pages << shift, cluster_k, scale_k, zero_k, cluster_v, scale_v, zero_v, g, bits,
+                      k_pages, v_pages, weights, d.err, (cudaStream_t)stream, d.num_sms};
+    return cuda_status(launch_paged_append(a));
+}
+
+int rptq_kv_paged_dequant(const uint8_t *pages, int H, int D, int bits, const int32_t *start,
+                          const int32_t *begin, int B, const int32_t *page_table, int max_pages,
+                          int64_t n_pages, int page_size, int64_t T, const int32_t *cluster,
+                          const float *scale, const int32_t *zero, int g, void *out, int out_dtype,
+                          rptq_stream_t stream)
+{
+    int shift;
+    if (!dtype_ok(out_dtype)) return RPTQ_ERR_UNSUPPORTED;
+    if (int st = paged_shape(H, D, bits, B, max_pages, n_pages, page_size, &shift)) return st;
+    if (T < 0 || g <= 0) return RPTQ_ERR_INVALID_ARG;
+    if (T > 0x7fffffffLL) return RPTQ_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0) return RPTQ_OK;
+    if (!pages || !start || !begin || !page_table || !cluster || !scale || !zero || !out) return RPTQ_ERR_INVALID_ARG;
+    if (!aligned16(pages) || !aligned16(out)) return RPTQ_ERR_INVALID_ARG;
+    DevInfo d;
+    int st = dev_info(&d);
+    if (st) return st;
+    PagedDequantArgs a{pages, H, D, bits, start, begin, page_table, B, max_pages, shift, n_pages, max_pages << shift,
+                       T, cluster, scale, zero, g, out, out_dtype, d.err, (cudaStream_t)stream, d.num_sms};
+    return cuda_status(launch_paged_dequant(a));
+}
+
+int rptq_kv_paged_evict(uint8_t *k_pages, uint8_t *v_pages, float *weights, int B, int H, int D,
+                        int bits, const int32_t *lens, const int32_t *page_table, int max_pages,
+                        int64_t n_pages, int page_size, int max_len, int budget, int recent,
+                        int32_t *new_lens, int32_t *kept, rptq_stream_t stream)
+{
+    int shift;
+    if (int st = paged_shape(H, D, bits, B, max_pages, n_pages, page_size, &shift)) return st;
+    if (budget < 1 || recent < 0 || recent > budget || max_len < 0 || max_len > ((int64_t)max_pages << shift))
+        return RPTQ_ERR_INVALID_ARG;
+    if (B == 0) return RPTQ_OK;
+    if (!k_pages || !v_pages || !weights || !lens || !page_table || !new_lens || !kept) return RPTQ_ERR_INVALID_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages)) return RPTQ_ERR_INVALID_ARG;
+    if (new_lens < lens + B && lens < new_lens + B) return RPTQ_ERR_INVALID_ARG;  // every head reads lens
+    DevInfo d;
+    int st = dev_info(&d);
+    if (st) return st;
+    PagedEvictArgs a{k_pages, v_pages, weights, B, H, D, bits, lens, page_table, max_pages, shift, n_pages,
+                     max_len, budget, recent, new_lens, kept, d.err, (cudaStream_t)stream, d.num_sms};
+    return cuda_status(launch_paged_evict(a));
+}
+
+size_t rptq_kv_paged_attention_workspace_size(int64_t T, int Hq, int H, int D, int dtype, int B,
+                                              int max_q, int max_len, int weights)
+{
+    if (T <= 0 || Hq <= 0 || H <= 0 || Hq % H != 0 || D <= 0 || !dtype_ok(dtype) || B <= 0 || max_q <= 0 || max_len <= 0)
+        return 0;
+    return paged_attention_workspace(T, Hq, weights);
+}
+
+int rptq_kv_paged_attention(const void *q, int dtype, int64_t T, int Hq, int H, int D, int64_t q_stride,
+                            const int32_t *start, const int32_t *lens, int B, int max_q, int max_len,
+                            const int32_t *page_table, int max_pages, int64_t n_pages, int page_size,
+                            const uint8_t *k_pages, const uint8_t *v_pages, const int32_t *cluster_k,
+                            const float *scale_k, const int32_t *zero_k, const int32_t *cluster_v,
+                            const float *scale_v, const int32_t *zero_v, int g, int bits, float scale,
+                            void *out, float *weights, void *workspace, size_t workspace_bytes,
+                            rptq_stream_t stream)
+{
+    int shift;
+    if (!dtype_ok(dtype)) return RPTQ_ERR_UNSUPPORTED;
+    if (int st = paged_shape(H, D, bits, B, max_pages, n_pages, page_size, &shift)) return st;
+    if (Hq < H || Hq % H != 0 || T < 0 || g <= 0 || max_q < 0 || max_len < 0 ||
+        max_len > ((int64_t)max_pages << shift) || !(scale >= 0.0f) || !(scale < INFINITY))
+        return RPTQ_ERR_INVALID_ARG;
+    if (q_stride < (int64_t)Hq * D || q_stride * esize(dtype) % 16 != 0) return RPTQ_ERR_INVALID_ARG;
+    if (T * Hq > 0x7fffffffLL || (int64_t)B * H * ((max_len + 3) / 4) > 0x7fffffffLL) return RPTQ_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0 || max_q == 0) return RPTQ_OK;
+    if (!q || !start || !lens || !page_table || !k_pages || !v_pages || !out || !cluster_k || !scale_k || !zero_k ||
+        !cluster_v || !scale_v || !zero_v)
+        return RPTQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_pages) || !aligned16(v_pages)) return RPTQ_ERR_INVALID_ARG;
+    const size_t need = rptq_kv_paged_attention_workspace_size(T, Hq, H, D, dtype, B, max_q, max_len, weights != nullptr);
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return RPTQ_ERR_WORKSPACE;
+    DevInfo d;
+    int st = dev_info(&d);
+    if (st) return st;
+    PagedAttnArgs a{q, dtype, T, Hq, H, D, q_stride, start, lens, page_table, B, max_pages, shift, n_pages, max_q,
+                    max_len, k_pages, v_pages,
+                    KvTables{cluster_k, scale_k, zero_k, cluster_v, scale_v, zero_v, g}, bits,
+                    scale > 0.f ? scale : 1.0f / sqrtf((float)D), out, weights, workspace, d.err,
+                    (cudaStream_t)stream, d.num_sms};
+    return cuda_status(launch_paged_attention(a));
+}
+
 int rptq_baseline_explicit_reorder_quant(const void *x, int dtype, int64_t T, int C,
                                          const float *gamma, const float *beta, float eps,
                                          const int32_t *R, const int32_t *col_cluster,

@@ -1,0 +1,427 @@
+// kv_paged.cu -- the paged packed K/V cache: tokens quantized into pages, read back, and evicted.
+//
+// RPTQ article (基于重排序的新量化方法RPTQ…), results paragraph (the K and V caches quantized per
+// cluster) and closing memory paragraph (the cache dominates memory at large batch x sequence): the
+// same codes as the dense cache's, in pages, so that sequences of unequal length share one pool
+// (kv_paged.cuh has the layout).
+#include <algorithm>
+
+#include "kv_codec.cuh"
+#include "kv_paged.cuh"
+#include "launch.h"
+
+namespace rptq {
+
+// ---- append and read-back ------------------------------------------------------------------------
+// A thread owns 8 consecutive channels, whose coefficients stay in registers, and walks the rows of
+// its CTA's chunk of the batch; blockIdx.y is the slab of blockDim.x * 8 channels, blockIdx.z the
+// tensor.  Where each row of the chunk lives is looked up once per CTA.  Both directions move each
+// byte once and are bound by HBM at large batches and by the launch at small ones.
+constexpr int PG_THREADS = 256;
+constexpr int PG_ROWS = 64;  // most rows of a CTA's chunk
+constexpr int PG_UNROLL = 4;  // rows whose loads are in flight together
+
+// Four lanes' 24-bit groups <-> the three 32-bit words they fill (lane j of the four holds word j < 3).
+__device__ __forceinline__ uint32_t pack_a3_words(uint32_t grp, int lane)
+{
+    const uint32_t next = __shfl_down_sync(FULL, grp, 1);
+    const int j = lane & 3;
+    return (grp >> (8 * j)) | (next << (24 - 8 * j));
+}
+__device__ __forceinline__ uint32_t unpack_a3_words(uint32_t w, int lane)
+{
+    const int j = lane & 3, base = lane & ~3;
+    const uint32_t lo = __shfl_sync(FULL, w, base + (j == 3 ? 2 : max(j - 1, 0)));
+    const uint32_t hi = __shfl_sync(FULL, w, base + min(j, 2));
+    // group j is bits 24j .. 24j + 23 of the 96: words (0), (0, 1), (1, 2), (2)
+    return j == 0 ? lo : j == 3 ? lo >> 8 : __funnelshift_r(lo, hi, 32 - 8 * j);
+}
+
+template <typename T, int BITS>
+__global__ void __launch_bounds__(PG_THREADS)
+    kv_paged_append_kernel(KvTensors t, Paged p, int64_t row_stride, int H, int D, int g, int rows_per_cta,
+                           float *__restrict__ weights)
+{
+    constexpr int VEC = Elem<T>::VEC, NLD = 8 / VEC;
+    __shared__ int s_page[PG_ROWS], s_slot[PG_ROWS];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const T *src = static_cast<const T *>(t.src[blockIdx.z]);
+    if (src == nullptr) return;
+    uint8_t *dst = t.dst[blockIdx.z];
+    const int64_t t0 = (int64_t)blockIdx.x * rows_per_cta;
+    const int rows = (int)min((int64_t)rows_per_cta, p.T - t0);
+    if (tid < rows) {
+        int page = -1, slot = 0;
+        const int b = paged_row_sequence(p, t0 + tid);
+        int s0, n, L;
+        if (b >= 0 && paged_sequence(p, b, s0, n, L)) {
+            const int pos = L - n + (int)(t0 + tid - s0);
+            if (pos >= 0) {
+                page = paged_page(p, b, pos >> p.shift);
+                slot = pos & ((1 << p.shift) - 1);
+            }
+        }
+        s_page[tid] = page;
+        s_slot[tid] = slot;
+    }
+    const int c0 = (blockIdx.y * blockDim.x + tid) * 8;
+    const bool live = c0 < H * D;
+    const int c = live ? c0 : 0, h = c / D, d0 = c - h * D;
+    KvCoef<BITS, 8> cf;
+    cf.load(t.cl[blockIdx.z], t.sc[blockIdx.z], t.zp[blockIdx.z], c, g, p.err);
+    __syncthreads();
+    const int rb = D * BITS / 8;
+    for (int i0 = 0; i0 < rows; i0 += PG_UNROLL) {
+        uint4 x[PG_UNROLL][NLD];
+#pragma unroll
+        for (int u = 0; u < PG_UNROLL; ++u)
+#pragma unroll
+            for (int l = 0; l < NLD; ++l)
+                x[u][l] = i0 + u < rows ? ldg_stream(src + (t0 + i0 + u) * row_stride + c + l * VEC) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < PG_UNROLL; ++u) {
+            const int i = i0 + u;
+            if (i >= rows) break;
+            uint32_t grp[1];
+            kv_quant_row<T, BITS, 8>(x[u], cf, grp);
+            const uint32_t w = BITS == 4 ? grp[0] : pack_a3_words(grp[0], lane);
+            if (!live || s_page[i] < 0) continue;
+            const int64_t row = paged_row(s_page[i], H, h, p.shift) + s_slot[i];
+            if (BITS == 4)
+                *reinterpret_cast<uint32_t *>(dst + row * rb + d0 / 2) = w;
+            else if ((lane & 3) < 3)
+                *reinterpret_cast<uint32_t *>(dst + row * rb + (d0 & ~31) * 3 / 8 + (lane & 3) * 4) = w;
+            if (weights != nullptr && blockIdx.z == 0 && d0 == 0) weights[row] = 0.f;
+        }
+    }
+}
+
+template <typename T> __device__ __forceinline__ void store8(T *dst, const float (&v)[8]);
+template <> __device__ __forceinline__ void store8<float>(float *dst, const float (&v)[8])
+{
+    __stcs(reinterpret_cast<float4 *>(dst), make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(reinterpret_cast<float4 *>(dst) + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+template <> __device__ __forceinline__ void store8<__half>(__half *dst, const float (&v)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+}
+template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16 *dst, const float (&v)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+template <typename T, int BITS>
+__global__ void __launch_bounds__(PG_THREADS)
+    kv_paged_dequant_kernel(const uint8_t *__restrict__ pages, Paged p, int H, int D, const int32_t *__restrict__ cluster,
+                            const float *__restrict__ scale, const int32_t *__restrict__ zero, int g, int rows_per_cta,
+                            T *__restrict__ out)
+{
+    constexpr uint32_t MASK = (1u << BITS) - 1u;
+    __shared__ int s_page[PG_ROWS], s_slot[PG_ROWS];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t t0 = (int64_t)blockIdx.x * rows_per_cta;
+    const int rows = (int)min((int64_t)rows_per_cta, p.T - t0);
+    if (tid < rows) {
+        int page = -1, slot = 0;
+        const int b = paged_row_sequence(p, t0 + tid);
+        if (b >= 0) {  // p.lens: the first position read of each sequence
+            const int64_t pos = (int64_t)p.lens[b] + (t0 + tid - p.start[b]);
+            if (pos >= 0 && pos < p.max_len) {
+                page = paged_page(p, b, (int)(pos >> p.shift));
+                slot = (int)pos & ((1 << p.shift) - 1);
+            } else {
+                raise_error(p.err, RPTQ_DEVERR_RANGE);
+            }
+        }
+        s_page[tid] = page;
+        s_slot[tid] = slot;
+    }
+    const int c0 = (blockIdx.y * blockDim.x + tid) * 8;
+    const bool live = c0 < H * D;
+    const int c = live ? c0 : 0, h = c / D, d0 = c - h * D;
+    float s[8];
+    int z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        int k = cluster[c + i];
+        if (k < 0 || k >= g) {
+            raise_error(p.err, RPTQ_DEVERR_CLUSTER_ID);
+            k = 0;
+        }
+        s[i] = scale[k];
+        z[i] = zero[k];
+    }
+    __syncthreads();
+    const int rb = D * BITS / 8;
+    const int off = BITS == 4 ? d0 / 2 : (d0 & ~31) * 3 / 8 + min(lane & 3, 2) * 4;
+    for (int i0 = 0; i0 < rows; i0 += PG_UNROLL) {
+        uint32_t w[PG_UNROLL];
+#pragma unroll
+        for (int u = 0; u < PG_UNROLL; ++u) {
+            const int i = min(i0 + u, rows - 1);
+            const int64_t row = paged_row(max(s_page[i], 0), H, h, p.shift) + s_slot[i];
+            w[u] = ldg_stream32(pages + row * rb + off);
+        }
+#pragma unroll
+        for (int u = 0; u < PG_UNROLL; ++u) {
+            const int i = i0 + u;
+            if (i >= rows) break;
+            const uint32_t grp = BITS == 4 ? w[u] : unpack_a3_words(w[u], lane);
+            if (!live || s_page[i] < 0) continue;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = s[j] * (float)((int)((grp >> (BITS * j)) & MASK) - z[j]);
+            store8(out + (t0 + i) * H * D + c, v);
+        }
+    }
+}
+
+// Rows of a CTA: as many as leave about two CTAs for every SM, at most PG_ROWS.
+static void paged_rows_grid(int64_t T, int C, int tensors, int num_sms, int *threads, int *rows, dim3 *grid)
+{
+    *threads = std::min(PG_THREADS, (C / 8 + 31) / 32 * 32);
+    const int slabs = (C / 8 + *threads - 1) / *threads;
+    const int64_t want = T * slabs * tensors / (2 * num_sms);
+    *rows = (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min(PG_ROWS, *threads)));
+    *grid = dim3((unsigned)((T + *rows - 1) / *rows), (unsigned)slabs, (unsigned)tensors);
+}
+
+template <typename T>
+static cudaError_t launch_paged_append_t(const PagedAppendArgs &a)
+{
+    const KvTensors t{{a.k, a.v}, {a.kq, a.vq}, {a.ck, a.cv}, {a.sk, a.sv}, {a.zk, a.zv}};
+    const Paged p{a.start, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, 0x7fffffff, a.max_len, a.err};
+    int threads, rows;
+    dim3 grid;
+    paged_rows_grid(a.T, a.H * a.D, 2, a.num_sms, &threads, &rows, &grid);
+    if (a.bits == 4)
+        kv_paged_append_kernel<T, 4><<<grid, threads, 0, a.stream>>>(t, p, a.row_stride, a.H, a.D, a.g, rows, a.weights);
+    else
+        kv_paged_append_kernel<T, 3><<<grid, threads, 0, a.stream>>>(t, p, a.row_stride, a.H, a.D, a.g, rows, a.weights);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_paged_append(const PagedAppendArgs &a)
+{
+    switch (a.dtype) {
+    case RPTQ_F32: return launch_paged_append_t<float>(a);
+    case RPTQ_F16: return launch_paged_append_t<__half>(a);
+    default: return launch_paged_append_t<__nv_bfloat16>(a);
+    }
+}
+
+template <typename T>
+static cudaError_t launch_paged_dequant_t(const PagedDequantArgs &a)
+{
+    const Paged p{a.start, a.begin, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, 0x7fffffff, a.max_len, a.err};
+    int threads, rows;
+    dim3 grid;
+    paged_rows_grid(a.T, a.H * a.D, 1, a.num_sms, &threads, &rows, &grid);
+    T *out = static_cast<T *>(a.out);
+    if (a.bits == 4)
+        kv_paged_dequant_kernel<T, 4><<<grid, threads, 0, a.stream>>>(a.pages, p, a.H, a.D, a.cluster, a.scale, a.zero,
+                                                                      a.g, rows, out);
+    else
+        kv_paged_dequant_kernel<T, 3><<<grid, threads, 0, a.stream>>>(a.pages, p, a.H, a.D, a.cluster, a.scale, a.zero,
+                                                                      a.g, rows, out);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_paged_dequant(const PagedDequantArgs &a)
+{
+    switch (a.out_dtype) {
+    case RPTQ_F32: return launch_paged_dequant_t<float>(a);
+    case RPTQ_F16: return launch_paged_dequant_t<__half>(a);
+    default: return launch_paged_dequant_t<__nv_bfloat16>(a);
+    }
+}
+
+// ---- eviction --------------------------------------------------------------------------------------
+// One CTA per (sequence, head).  The weights' order is that of an unsigned key; the key of the m-th
+// largest candidate is found by four passes of an 8-bit histogram from the top byte down (a radix
+// select), `ties` of the candidates equal to it are kept, lowest positions first.  Two passes over the
+// positions, every warp over its own contiguous range, then count and write the kept positions in
+// order.  Entry j of that list moves from position kept[j] >= j to j: a batch of rows is loaded by the
+// whole CTA, then stored.  A row stored at j < i is never one that a later entry i reads (kept[i] >= i),
+// so the only hazard is inside a batch, and one barrier between its loads and stores covers it.
+constexpr int EV_THREADS = 1024, EV_WARPS = EV_THREADS / 32;
+constexpr int EV_UNITS = 4;  // units of a batch per thread
+
+// Larger weight, larger key; both zeros alike; NaN below everything.
+__device__ __forceinline__ uint32_t weight_key(float w)
+{
+    const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
+    if (w != w) return 0u;
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+template <typename U>
+__global__ void __launch_bounds__(EV_THREADS)
+    kv_paged_evict_kernel(uint8_t *__restrict__ kq, uint8_t *__restrict__ vq, float *__restrict__ weights, Paged p, int H,
+                          int rb, int budget, int recent, int32_t *__restrict__ new_lens, int32_t *__restrict__ kept)
+{
+    __shared__ int hist[256];
+    __shared__ int s_eq[EV_WARPS], s_keep[EV_WARPS], s_digit, s_need, s_bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / H, h = blockIdx.x % H;
+    int32_t *list = kept + (int64_t)blockIdx.x * budget;
+    const int L = p.lens[b];
+    const int32_t *tab = p.table + (int64_t)b * p.max_pages;
+    const int pmask = (1 << p.shift) - 1;
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    bool bad = L < 0 || L > p.max_len;
+    if (bad && tid == 0) raise_error(p.err, RPTQ_DEVERR_RANGE);
+    if (!bad && L > budget)  // an evicted sequence's pages are all checked before anything moves
+        for (int i = tid; i < (L + pmask) >> p.shift; i += EV_THREADS)
+            if (paged_page(p, b, i) < 0) s_bad = 1;
+    __syncthreads();
+    bad |= s_bad != 0;
+    if (h == 0 && tid == 0) new_lens[b] = bad ? L : min(L, budget);
+    if (bad || L <= budget) {
+        const int n = bad ? 0 : L;
+        for (int j = tid; j < budget; j += EV_THREADS) list[j] = j < n ? j : -1;
+        return;
+    }
+    auto row_of = [&](int pos) -> int64_t { return paged_row(tab[pos >> p.shift], H, h, p.shift) + (pos & pmask); };
+    const int cand = L - recent;  // candidates; budget - recent of them stay
+    uint32_t prefix = 0, mask = 0;
+    int need = budget - recent;
+    for (int sh = 24; sh >= 0 && need > 0; sh -= 8) {
+        for (int i = tid; i < 256; i += EV_THREADS) hist[i] = 0;
+        __syncthreads();
+        for (int i0 = warp * 32; i0 < cand; i0 += EV_THREADS) {
+            const int pos = i0 + lane;
+            const uint32_t key = pos < cand ? weight_key(weights[row_of(pos)]) : 0u;
+            const bool in = pos < cand && (key & mask) == prefix;
+            const uint32_t digit = in ? (key >> sh) & 255u : 256u;
+            const uint32_t same = __match_any_sync(FULL, digit);
+            if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+        }
+        __syncthreads();
+        if (warp == 0) {  // lane l: bins 255 - 8l .. 248 - 8l; the digit where the count from the top reaches need
+            int c[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
+            int before = sum;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(FULL, before, o);
+                if (lane >= o) before += v;
+            }
+            before -= sum;
+            if (before < need && before + sum >= need) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (before < need && before + c[i] >= need) {
+                        s_digit = 255 - 8 * lane - i;
+                        s_need = need - before;
+                        break;
+                    }
+                    before += c[i];
+                }
+            }
+        }
+        __syncthreads();
+        prefix |= (uint32_t)s_digit << sh;
+        mask |= 255u << sh;
+        need = s_need;
+    }
+    const bool some = budget > recent;  // else no candidate stays
+    const int ties = need;
+    // warp w: positions [w0, w1)
+    const int per = ((L + EV_WARPS - 1) / EV_WARPS + 31) & ~31;
+    const int w0 = min(L, warp * per), w1 = min(L, w0 + per);
+    int n_eq = 0, n_gt = 0;  // candidates equal to the threshold; those above it and the recent ones
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int pos = i0 + lane;
+        const uint32_t key = pos < cand && pos < w1 ? weight_key(weights[row_of(pos)]) : 0u;
+        const bool c = pos < cand && pos < w1 && some;
+        n_eq += __popc(__ballot_sync(FULL, c && key == prefix));
+        n_gt += __popc(__ballot_sync(FULL, (c && key > prefix) || (pos >= cand && pos < w1)));
+    }
+    if (lane == 0) s_eq[warp] = n_eq;
+    __syncthreads();
+    int eq = 0;  // equal candidates before this warp's range
+    for (int w = 0; w < warp; ++w) eq += s_eq[w];
+    if (lane == 0) s_keep[warp] = n_gt + max(0, min(n_eq, ties - eq));
+    __syncthreads();
+    int at = 0;
+    for (int w = 0; w < warp; ++w) at += s_keep[w];
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int pos = i0 + lane;
+        const uint32_t key = pos < cand && pos < w1 ? weight_key(weights[row_of(pos)]) : 0u;
+        const bool c = pos < cand && pos < w1 && some;
+        const uint32_t be = __ballot_sync(FULL, c && key == prefix), below = (1u << lane) - 1u;
+        const bool keep = (c && key > prefix) || (pos >= cand && pos < w1) ||
+                          (c && key == prefix && eq + __popc(be & below) < ties);
+        const uint32_t bk = __ballot_sync(FULL, keep);
+        if (keep) list[at + __popc(bk & below)] = pos;
+        eq += __popc(be);
+        at += __popc(bk);
+    }
+    __syncthreads();
+    // move: units of sizeof(U) bytes, `per_row` to a row of K or V
+    const int per_row = rb / (int)sizeof(U);
+    const int units = 2 * per_row;
+    const int64_t total = (int64_t)budget * units;
+    for (int64_t u0 = 0; u0 < total; u0 += EV_THREADS * EV_UNITS) {
+        U v[EV_UNITS];
+        U *to[EV_UNITS];
+#pragma unroll
+        for (int k = 0; k < EV_UNITS; ++k) {
+            const int64_t u = u0 + k * EV_THREADS + tid;
+            to[k] = nullptr;
+            if (u < total) {
+                const int j = (int)(u / units), part = (int)(u - (int64_t)j * units);
+                const int pos = list[j];
+                if (pos != j) {
+                    uint8_t *base = part < per_row ? kq : vq;
+                    const int o = part < per_row ? part : part - per_row;
+                    v[k] = *(reinterpret_cast<const U *>(base + row_of(pos) * rb) + o);
+                    to[k] = reinterpret_cast<U *>(base + row_of(j) * rb) + o;
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < EV_UNITS; ++k)
+            if (to[k] != nullptr) *to[k] = v[k];
+    }
+    for (int j0 = 0; j0 < budget; j0 += EV_THREADS) {
+        const int j = j0 + tid;
+        const int pos = j < budget ? list[j] : 0;
+        const bool moves = j < budget && pos != j;
+        const float w = moves ? weights[row_of(pos)] : 0.f;
+        __syncthreads();
+        if (moves) weights[row_of(j)] = w;
+    }
+}
+
+cudaError_t launch_paged_evict(const PagedEvictArgs &a)
+{
+    const Paged p{nullptr, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, 0, 0, a.max_len, a.err};
+    const int rb = a.D * a.bits / 8;
+    const unsigned grid = (unsigned)(a.B * a.H);
+    if (rb % 16 == 0)
+        kv_paged_evict_kernel<uint4><<<grid, EV_THREADS, 0, a.stream>>>(a.kq, a.vq, a.weights, p, a.H, rb, a.budget,
+                                                                        a.recent, a.new_lens, a.kept);
+    else
+        kv_paged_evict_kernel<uint32_t><<<grid, EV_THREADS, 0, a.stream>>>(a.kq, a.vq, a.weights, p, a.H, rb, a.budget,
+                                                                           a.recent, a.new_lens, a.kept);
+    return cudaGetLastError();
+}
+
+}  // namespace rptq

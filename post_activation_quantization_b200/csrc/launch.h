@@ -177,6 +177,96 @@ struct LinArgs {
     cudaStream_t stream;
 };
 
+// The paged K/V cache (kv_paged.cuh): start [B + 1], lens [B], table [B, max_pages], P = 1 << shift.
+struct PagedAppendArgs {
+    const void *k, *v;
+    int dtype;
+    int64_t T, row_stride;
+    int H, D;
+    const int32_t *start, *lens, *table;
+    int B, max_pages, shift;
+    int64_t n_pages;
+    int max_len;
+    const int32_t *ck;
+    const float *sk;
+    const int32_t *zk;
+    const int32_t *cv;
+    const float *sv;
+    const int32_t *zv;
+    int g, bits;
+    uint8_t *kq, *vq;
+    float *weights;
+    int *err;
+    cudaStream_t stream;
+    int num_sms;
+};
+
+struct PagedDequantArgs {
+    const uint8_t *pages;
+    int H, D, bits;
+    const int32_t *start, *begin, *table;
+    int B, max_pages, shift;
+    int64_t n_pages;
+    int max_len;
+    int64_t T;
+    const int32_t *cluster;
+    const float *scale;
+    const int32_t *zero;
+    int g;
+    void *out;
+    int out_dtype;
+    int *err;
+    cudaStream_t stream;
+    int num_sms;
+};
+
+struct PagedEvictArgs {
+    uint8_t *kq, *vq;
+    float *weights;
+    int B, H, D, bits;
+    const int32_t *lens, *table;
+    int max_pages, shift;
+    int64_t n_pages;
+    int max_len, budget, recent;
+    int32_t *new_lens, *kept;
+    int *err;
+    cudaStream_t stream;
+    int num_sms;
+};
+
+// the clusters of K's and V's channels
+struct KvTables {
+    const int32_t *ck;
+    const float *sk;
+    const int32_t *zk;
+    const int32_t *cv;
+    const float *sv;
+    const int32_t *zv;
+    int g;
+};
+
+struct PagedAttnArgs {
+    const void *q;
+    int dtype;
+    int64_t T;
+    int Hq, H, D;
+    int64_t q_stride;
+    const int32_t *start, *lens, *table;
+    int B, max_pages, shift;
+    int64_t n_pages;
+    int max_q, max_len;
+    const uint8_t *kq, *vq;
+    KvTables kt;
+    int bits;
+    float scale;
+    void *out;
+    float *weights;
+    void *ws;
+    int *err;
+    cudaStream_t stream;
+    int num_sms;
+};
+
 struct DequantArgs {
     const uint8_t *codes;
     int layout;
@@ -229,6 +319,11 @@ cudaError_t launch_kv_attention(const KvAttnArgs &a);
 cudaError_t launch_kv_quant_reordered(const KvReorderedArgs &a);
 // (H, D, g) that the cluster-ordered K/V kernel takes, with its tables within max_smem
 bool kv_quant_reordered_supported(int H, int D, int g, int max_smem);
+cudaError_t launch_paged_append(const PagedAppendArgs &a);
+cudaError_t launch_paged_dequant(const PagedDequantArgs &a);
+cudaError_t launch_paged_evict(const PagedEvictArgs &a);
+cudaError_t launch_paged_attention(const PagedAttnArgs &a);
+size_t paged_attention_workspace(int64_t T, int Hq, int weights);
 cudaError_t launch_linear_prepare(const LinPrepArgs &a);
 cudaError_t launch_reordered_linear(const LinArgs &a);
 // largest number of cache positions one decode-attention call reads (its scores stay in shared

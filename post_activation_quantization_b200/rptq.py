@@ -24,8 +24,10 @@ RPTQ_ERR_DEVICE = -5
 RPTQ_F32, RPTQ_F16, RPTQ_BF16 = 0, 1, 2
 RPTQ_LAYOUT_ROWS, RPTQ_LAYOUT_BHSD = 0, 1
 RPTQ_DEVERR_CLUSTER_ID, RPTQ_DEVERR_REORDER, RPTQ_DEVERR_TIMEOUT = 1, 2, 4
+RPTQ_DEVERR_PAGE, RPTQ_DEVERR_RANGE = 8, 16
 RPTQ_MAX_CHANNELS = 16384
 RPTQ_MAX_CLUSTERS = 512
+RPTQ_MAX_POSITIONS = 1 << 30
 
 _DT = {torch.float32: RPTQ_F32, torch.float16: RPTQ_F16, torch.bfloat16: RPTQ_BF16}
 _TD = {v: k for k, v in _DT.items()}
@@ -58,6 +60,13 @@ SIGNATURES = {
     "rptq_ln_reorder_quant_planned": (_I, [_P, _I, _I64, _I, _F, _P, _I, _P, _P]),
     "rptq_linear_prepare": (_I, [_P, _P, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P, _P]),
     "rptq_reordered_linear": (_I, [_P, _I64, _I, _I, _P, _P, _P, _P, _I, _P, _P]),
+    "rptq_kv_paged_append": (_I, [_P, _P, _I, _I64, _I, _I, _I64, _P, _P, _I, _P, _I, _I64, _I, _P, _P, _P, _P, _P, _P,
+                                  _I, _I, _P, _P, _P, _P]),
+    "rptq_kv_paged_dequant": (_I, [_P, _I, _I, _I, _P, _P, _I, _P, _I, _I64, _I, _I64, _P, _P, _P, _I, _P, _I, _P]),
+    "rptq_kv_paged_attention_workspace_size": (_SZ, [_I64, _I, _I, _I, _I, _I, _I, _I, _I]),
+    "rptq_kv_paged_attention": (_I, [_P, _I, _I64, _I, _I, _I, _I64, _P, _P, _I, _I, _I, _P, _I, _I64, _I, _P, _P, _P, _P,
+                                     _P, _P, _P, _P, _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "rptq_kv_paged_evict": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _I64, _I, _I, _I, _I, _P, _P, _P]),
     # include/rptq_baseline.h
     "rptq_baseline_explicit_reorder_quant": (_I, [_P, _I, _I64, _I, _P, _P, _F, _P, _P, _P, _P, _I, _I, _P, _P, _P,
                                                   _P]),
@@ -369,6 +378,159 @@ def rptq_reordered_linear(codes, C: int, bits: int, w_prep, w_bias, w_lambda, w_
                                      _ptr(w_scale), N, _ptr(out), _stream(stream))
     _check(st, "rptq_reordered_linear")
     return out
+
+
+# ---------------------------------------------------------------------------------------------
+# The paged packed K/V cache
+def _need(ok, where: str):
+    if not ok:
+        raise RptqError(RPTQ_ERR_INVALID_ARG, where)
+
+
+def _arg(t: torch.Tensor | None, dtype, shape, dev, where: str, rows: bool = False):
+    """Address of a tensor that must have this type, shape (None: any) and device; contiguous, or
+    (rows) [T, heads, D] whose rows may be further apart than one row."""
+    if t is None:
+        return None
+    ok = t.dtype == dtype and t.device == dev and t.dim() == len(shape) and all(
+        s is None or s == x for s, x in zip(shape, t.shape))
+    if rows:
+        ok = ok and (t.numel() == 0 or (t.stride(2) == 1 and t.stride(1) == t.shape[2]))
+    else:
+        ok = ok and t.is_contiguous()
+    _need(ok, where)
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _paged(pages: torch.Tensor, page_table: torch.Tensor, bits: int, where: str):
+    """(device, H, D, B, max_pages, n_pages, page_size) of a pool and its page table."""
+    _need(pages.dim() == 4 and page_table.dim() == 2 and pages.is_cuda, where)
+    dev = pages.device
+    _need(dev.index == torch.cuda.current_device(), where)
+    n_pages, H, P, rb = pages.shape
+    _need(bits > 0 and rb * 8 % bits == 0, where)
+    return dev, H, rb * 8 // bits, page_table.shape[0], page_table.shape[1], n_pages, P
+
+
+def _clusters(cluster, scale, zero, C: int, dev, where: str):
+    """Addresses of one tensor's (cluster, scale, zero) and its cluster count."""
+    g = scale.numel()
+    return (_arg(cluster, torch.int32, (C,), dev, where), _arg(scale, torch.float32, (g,), dev, where),
+            _arg(zero, torch.int32, (g,), dev, where)), g
+
+
+def rptq_kv_paged_append(k_new, v_new, start, lens, page_table, k_pages, v_pages, cluster_k, scale_k, zero_k, cluster_v,
+                         scale_v, zero_v, bits: int, weights=None, stream=None):
+    """Quantize a ragged batch of new tokens [T, H, D] (either may be None; rows may be slices of a
+    wider tensor) into the pages at the end of their sequences, in place; `weights`' new positions
+    become 0."""
+    w = "rptq_kv_paged_append"
+    x, pool = (k_new, k_pages) if k_new is not None else (v_new, v_pages)
+    _need(x is not None and pool is not None and x.dtype in _DT, w)
+    dev, H, D, B, max_pages, n_pages, P = _paged(pool, page_table, bits, w)
+    T = x.shape[0]
+    ck, cv, g = (None,) * 3, (None,) * 3, set()
+    if k_new is not None:
+        ck, n = _clusters(cluster_k, scale_k, zero_k, H * D, dev, w)
+        g.add(n)
+    if v_new is not None:
+        cv, n = _clusters(cluster_v, scale_v, zero_v, H * D, dev, w)
+        g.add(n)
+    _need(len(g) == 1, w)
+    if k_new is not None and v_new is not None:
+        _need(T < 2 or k_new.stride(0) == v_new.stride(0), w)
+    st = lib().rptq_kv_paged_append(
+        _arg(k_new, x.dtype, (T, H, D), dev, w, True), _arg(v_new, x.dtype, (T, H, D), dev, w, True), _DT[x.dtype], T, H, D,
+        _row_stride(x), _arg(start, torch.int32, (B + 1,), dev, w), _arg(lens, torch.int32, (B,), dev, w), B,
+        _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages, P, *ck, *cv, g.pop(), bits,
+        _arg(k_pages, torch.uint8, pool.shape, dev, w) if k_new is not None else None,
+        _arg(v_pages, torch.uint8, pool.shape, dev, w) if v_new is not None else None,
+        _arg(weights, torch.float32, (n_pages, H, P), dev, w), _stream(stream))
+    _check(st, w)
+    return k_pages, v_pages
+
+
+def rptq_kv_paged_dequant(pages, page_table, start, begin, cluster, scale, zero, bits: int, T: int | None = None, out=None,
+                          out_dtype=torch.float32, stream=None):
+    """Positions begin[b] + i of sequence b read back into row start[b] + i of [T, H, D].  T: the rows
+    (a host value; without it, out's)."""
+    w = "rptq_kv_paged_dequant"
+    dev, H, D, B, max_pages, n_pages, P = _paged(pages, page_table, bits, w)
+    if out is None:
+        _need(T is not None, w)
+        out = torch.empty((T, H, D), dtype=out_dtype, device=dev)
+    _need(out.dtype in _DT, w)
+    cl, g = _clusters(cluster, scale, zero, H * D, dev, w)
+    T = out.shape[0]
+    st = lib().rptq_kv_paged_dequant(
+        _arg(pages, torch.uint8, pages.shape, dev, w), H, D, bits, _arg(start, torch.int32, (B + 1,), dev, w),
+        _arg(begin, torch.int32, (B,), dev, w), B, _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages,
+        P, T, *cl, g, _arg(out, out.dtype, (T, H, D), dev, w), _DT[out.dtype], _stream(stream))
+    _check(st, w)
+    return out
+
+
+def rptq_kv_paged_attention_workspace_size(T: int, Hq: int, H: int, D: int, dtype, B: int, max_q: int, max_len: int,
+                                           weights: bool) -> int:
+    return int(lib().rptq_kv_paged_attention_workspace_size(T, Hq, H, D, _DT[dtype], B, max_q, max_len, int(bool(weights))))
+
+
+def rptq_kv_paged_attention(q, start, lens, page_table, k_pages, v_pages, cluster_k, scale_k, zero_k, cluster_v, scale_v,
+                            zero_v, bits: int, max_q: int, max_len: int, scale: float = 0.0, out=None, weights=None,
+                            workspace=None, stream=None):
+    """Causal attention of each sequence's newest tokens q [T, Hq, D] (rows may be slices of a wider
+    tensor) over all its positions; `weights` [n_pages, H, P], where given, grows by the positions'
+    attention weights."""
+    w = "rptq_kv_paged_attention"
+    dev, H, D, B, max_pages, n_pages, P = _paged(k_pages, page_table, bits, w)
+    _need(q.dtype in _DT and q.dim() == 3, w)
+    T, Hq, _ = q.shape
+    dt = _DT[q.dtype]
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+    L = lib()
+    ws_bytes = L.rptq_kv_paged_attention_workspace_size(T, Hq, H, D, dt, B, max_q, max_len, weights is not None)
+    if workspace is None:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    elif workspace.numel() * workspace.element_size() < ws_bytes:
+        raise RptqError(RPTQ_ERR_WORKSPACE, w)
+    ck, g = _clusters(cluster_k, scale_k, zero_k, H * D, dev, w)
+    cv, gv = _clusters(cluster_v, scale_v, zero_v, H * D, dev, w)
+    _need(g == gv, w)
+    st = L.rptq_kv_paged_attention(
+        _arg(q, q.dtype, (T, Hq, D), dev, w, True), dt, T, Hq, H, D, _row_stride(q),
+        _arg(start, torch.int32, (B + 1,), dev, w), _arg(lens, torch.int32, (B,), dev, w), B, max_q, max_len,
+        _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages, P,
+        _arg(k_pages, torch.uint8, k_pages.shape, dev, w), _arg(v_pages, torch.uint8, k_pages.shape, dev, w), *ck, *cv, g, bits,
+        float(scale), _arg(out, q.dtype, (T, Hq, D), dev, w), _arg(weights, torch.float32, (n_pages, H, P), dev, w),
+        None if workspace is None else _arg(workspace, workspace.dtype, workspace.shape, dev, w),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, w)
+    return out
+
+
+def rptq_kv_paged_evict(k_pages, v_pages, weights, lens, page_table, bits: int, budget: int, recent: int = 0,
+                        max_len: int | None = None, new_lens=None, kept=None, stream=None):
+    """Cut every (sequence, head) to `budget` positions: the last `recent` and those of the largest
+    running sums, moved together in place.  Returns (new_lens [B], kept [B, H, budget])."""
+    w = "rptq_kv_paged_evict"
+    dev, H, D, B, max_pages, n_pages, P = _paged(k_pages, page_table, bits, w)
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    if kept is None:
+        kept = torch.empty((B, H, max(budget, 0)), dtype=torch.int32, device=dev)
+    st = lib().rptq_kv_paged_evict(
+        _arg(k_pages, torch.uint8, k_pages.shape, dev, w), _arg(v_pages, torch.uint8, k_pages.shape, dev, w),
+        _arg(weights, torch.float32, (n_pages, H, P), dev, w), B, H, D, bits, _arg(lens, torch.int32, (B,), dev, w),
+        _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages, P,
+        max_pages * P if max_len is None else max_len, budget, recent, _arg(new_lens, torch.int32, (B,), dev, w),
+        _arg(kept, torch.int32, (B, H, max(budget, 0)), dev, w), _stream(stream))
+    _check(st, w)
+    return new_lens, kept
 
 
 # ---------------------------------------------------------------------------------------------
