@@ -418,6 +418,9 @@ int rptq_kv_decode_attention(const float *q, int B, int H, int D, const uint8_t 
 
 // ---- the paged K/V cache ----------------------------------------------------------------------
 namespace {
+// The workspace's size must be the same wherever it is asked for, with or without a GPU.
+constexpr int B200_SMS = 148;
+
 // Sizes of a paged pool; on RPTQ_OK *shift is log2 of the page size.
 int paged_shape(int H, int D, int bits, int B, int max_pages, int64_t n_pages, int page_size, int *shift)
 {
@@ -511,7 +514,7 @@ size_t rptq_kv_paged_attention_workspace_size(int64_t T, int Hq, int H, int D, i
 {
     if (T <= 0 || Hq <= 0 || H <= 0 || Hq % H != 0 || D <= 0 || !dtype_ok(dtype) || B <= 0 || max_q <= 0 || max_len <= 0)
         return 0;
-    return paged_attention_workspace(T, Hq, weights);
+    return paged_attention_workspace(T, Hq, H, D, dtype, B, max_q, max_len, weights, B200_SMS);
 }
 
 int rptq_kv_paged_attention(const void *q, int dtype, int64_t T, int Hq, int H, int D, int64_t q_stride,
@@ -530,7 +533,7 @@ int rptq_kv_paged_attention(const void *q, int dtype, int64_t T, int Hq, int H, 
         max_len > ((int64_t)max_pages << shift) || !(scale >= 0.0f) || !(scale < INFINITY))
         return RPTQ_ERR_INVALID_ARG;
     if (q_stride < (int64_t)Hq * D || q_stride * esize(dtype) % 16 != 0) return RPTQ_ERR_INVALID_ARG;
-    if (T * Hq > 0x7fffffffLL || (int64_t)B * H * ((max_len + 3) / 4) > 0x7fffffffLL) return RPTQ_ERR_UNSUPPORTED;
+    if (T * Hq > 0x7fffffffLL || (int64_t)B * H * ((max_len + 3) / 4) + T * Hq > 0x7fffffffLL) return RPTQ_ERR_UNSUPPORTED;
     if (T == 0 || B == 0 || max_q == 0) return RPTQ_OK;
     if (!q || !start || !lens || !page_table || !k_pages || !v_pages || !out || !cluster_k || !scale_k || !zero_k ||
         !cluster_v || !scale_v || !zero_v)
@@ -545,7 +548,7 @@ int rptq_kv_paged_attention(const void *q, int dtype, int64_t T, int Hq, int H, 
                     max_len, k_pages, v_pages,
                     KvTables{cluster_k, scale_k, zero_k, cluster_v, scale_v, zero_v, g}, bits,
                     scale > 0.f ? scale : 1.0f / sqrtf((float)D), out, weights, workspace, d.err,
-                    (cudaStream_t)stream, d.num_sms};
+                    (cudaStream_t)stream, B200_SMS};
     return cuda_status(launch_paged_attention(a));
 }
 

@@ -7,21 +7,9 @@
 // grows by w_p summed over the sequence's rows and the head's group of query heads.
 #include <algorithm>
 
-#include "kv_paged.cuh"
-#include "launch.h"
+#include "kv_paged_attn.cuh"
 
 namespace rptq {
-
-constexpr float LOG2E = 1.4426950408889634f;
-
-template <typename T> __device__ __forceinline__ float to_f32(T v);
-template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 // ---- general kernels: every head size ----------------------------------------------------------------
 // A lane owns D / 32 consecutive channels of a row.
@@ -168,8 +156,11 @@ __global__ void __launch_bounds__(GA_THREADS)
     if (lane == 0) weights[row] += w;
 }
 
-size_t paged_attention_workspace(int64_t T, int Hq, int weights)
+size_t paged_attention_workspace(int64_t T, int Hq, int H, int D, int dtype, int B, int max_q, int max_len, int weights,
+                                 int num_sms)
 {
+    if (paged_decode_takes(Hq, H, D, dtype, max_q, weights))
+        return paged_decode_workspace(T, Hq, H, D, dtype, B, max_q, max_len, weights, num_sms);
     return weights ? (size_t)T * Hq * sizeof(float) : 0;
 }
 
@@ -190,6 +181,7 @@ static cudaError_t launch_paged_attention_t(const PagedAttnArgs &a)
 
 cudaError_t launch_paged_attention(const PagedAttnArgs &a)
 {
+    if (paged_decode_takes(a.Hq, a.H, a.D, a.dtype, a.max_q, a.weights != nullptr)) return launch_paged_decode(a);
     switch (a.dtype) {
     case RPTQ_F32: return a.bits == 4 ? launch_paged_attention_t<float, 4>(a) : launch_paged_attention_t<float, 3>(a);
     case RPTQ_F16: return a.bits == 4 ? launch_paged_attention_t<__half, 4>(a) : launch_paged_attention_t<__half, 3>(a);

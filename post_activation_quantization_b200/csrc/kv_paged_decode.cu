@@ -1,0 +1,729 @@
+// kv_paged_decode.cu -- paged attention of few query rows to a K/V head: decode steps, short chunks.
+//
+// Few rows make the packed codes the traffic (62 codes per clock and SM at 3 bits and 6.5 TB/s), and on
+// the FMA pipe a code costs more instructions than that rate leaves.  Here the codes are the A operand of
+// mma.sync.m16n8k16 (fp16, fp32 sums), taken from the packed bytes with one mask per two codes
+// (kv_paged_attn.cuh), and the query rows are its 8 columns:
+//     S [16 positions, 8 rows] = codes of K [16, D] x q'^T,       O [16 channels, 8 rows] = codes of V^T x w^T.
+// The order of the channels inside a K step, and of the positions inside a block of 16, is free, so both
+// operands are read from shared memory as they lie there.  Where the result must be good to fp32, or there
+// are at most four rows, the 8 columns are 4 rows in two fp16 parts each, which costs nothing then.
+//
+// A CTA is four warps; warp w of part s of a (sequence, K/V head) takes the tiles of 32 positions
+// s * 4 + w, + 4 * splits, ...  Each warp streams its tiles' K and V rows (contiguous in a page) with
+// bulk copies into a ring of its own, keeps its own running maximum and sum, and needs no other warp until
+// the end, when the CTA joins its warps.  With one part the CTA writes the output; else a second kernel joins
+// the parts, and adds the positions' weights to the running sums from the scores that the first one kept.
+#include <algorithm>
+
+#include "kv_paged_attn.cuh"
+
+namespace rptq {
+
+constexpr int DEC_WARPS = 4, DEC_THREADS = 32 * DEC_WARPS;
+constexpr int DEC_TILE = 32;    // positions of a warp's tile: two blocks of 16
+#ifndef STG
+#define STG 4
+#endif
+#ifndef MINB
+#define MINB 4
+#endif
+#ifndef PERSM
+#define PERSM 3
+#endif
+constexpr int DEC_STAGES = STG;   // tiles of a warp's ring
+// Weights are held as 2^y, y = x - m + DEC_PSHIFT for a reference m that follows the running maximum: y up to
+// DEC_YMAX fits fp16, and its smallest step is 2^-(24 + DEC_PSHIFT) of a weight at the reference.
+constexpr int DEC_PSHIFT = 5;
+constexpr float DEC_YMAX = 15.f;
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8 x 8 transpose of 16-bit elements across the warp
+__device__ __forceinline__ uint32_t mat_trans(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+// two codes (fp16 subnormals) times 2^14: exact, and normal numbers
+__device__ __forceinline__ uint32_t code_up(uint32_t v)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x74007400u));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
+
+// ---- K: one thread's D / 4 consecutive codes of a row as D / 8 pairs --------------------------------------
+// Pair i holds code code(i, 0) at bit pos(i, 0) of the low half and code code(i, 1) at pos(i, 1) of the high
+// one.  4-bit: word j gives (8j, 8j+4), (8j+1, 8j+5), ... at positions 0, 4, 0, 4.  3-bit: a 32-bit window whose
+// first code is c holds codes c, c+1, c+2 at bits 0, 3, 6 and c+6, c+7, c+8 at 18, 21, 24; two windows three codes
+// apart cover 12 codes; the last 8 (D = 128) or 4 (D = 64) are laid into the halves first.
+template <int BITS, int D>
+struct KPairs {
+    static constexpr int N = D / 8;
+    __host__ __device__ static constexpr int code(int i, int half)
+    {
+        if (BITS == 4) return 8 * (i / 4) + i % 4 + 4 * half;
+        if (i < (D == 128 ? 12 : 6)) return 12 * (i / 6) + 3 * (i % 6 / 3) + i % 3 + 6 * half;
+        return D == 128 ? 24 + (i - 12) + 4 * half : 12 + (i - 6) + 2 * half;
+    }
+    __host__ __device__ static constexpr int pos(int i, int half)
+    {
+        if (BITS == 4) return 4 * (i & 1);
+        if (i < (D == 128 ? 12 : 6)) return 3 * (i % 3) + 2 * half;
+        return D == 128 ? (i == 15 ? 0 : 3 * (i - 12)) : 3 * (i - 6);
+    }
+    // the packed codes of the lane's quarter of the row at `a`
+    __device__ __forceinline__ static void load(const uint8_t *a, int t, uint32_t (&x)[N])
+    {
+        if constexpr (BITS == 4) {
+            uint32_t w[D / 32];
+            if constexpr (D == 128) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(a + 16 * t);
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2 *>(a + 8 * t);
+                w[0] = v.x, w[1] = v.y;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                const uint32_t u = w[j] >> 8;
+                x[4 * j] = w[j] & 0x000F000Fu;
+                x[4 * j + 1] = w[j] & 0x00F000F0u;
+                x[4 * j + 2] = u & 0x000F000Fu;
+                x[4 * j + 3] = u & 0x00F000F0u;
+            }
+        } else if constexpr (D == 128) {
+            const uint8_t *p = a + 12 * t;
+            const uint32_t x0 = lds32(p), x1 = lds32(p + 4), x2 = lds32(p + 8);
+            window(x0, &x[0]);
+            window(__funnelshift_r(x0, x1, 9), &x[3]);
+            window(__funnelshift_r(x1, x2, 4), &x[6]);
+            window(__funnelshift_r(x1, x2, 13), &x[9]);
+            const uint32_t w = x2 >> 8;  // codes 24..31
+            const uint32_t u = (w & 0xFFFu) | ((w << 4) & 0xFFFFF000u);
+            x[12] = u & 0x00070007u;
+            x[13] = u & 0x00380038u;
+            x[14] = u & 0x01C001C0u;
+            x[15] = (u >> 9) & 0x00070007u;
+        } else {
+            const uint8_t *p = a + ((6 * t) & ~3);  // 48 bits at byte 6t
+            const uint32_t s = 16 * (t & 1);
+            const uint32_t wa = lds32(p), wb = lds32(p + 4);
+            const uint32_t y0 = __funnelshift_r(wa, wb, s), y1 = wb >> s;
+            window(y0, &x[0]);
+            window(__funnelshift_r(y0, y1, 9), &x[3]);
+            const uint32_t w = y1 >> 4;  // codes 12..15
+            const uint32_t u = (w & 0x3Fu) | ((w << 10) & 0xFFFF0000u);
+            x[6] = u & 0x00070007u;
+            x[7] = u & 0x00380038u;
+        }
+    }
+    __device__ __forceinline__ static void window(uint32_t w, uint32_t *x)
+    {
+        x[0] = w & 0x001C0007u;
+        x[1] = w & 0x00E00038u;
+        x[2] = w & 0x070001C0u;
+    }
+};
+
+// ---- V: one thread's D / 8 consecutive codes of two rows, code by code -----------------------------------
+// x[i] holds code i of row a in the low half and of row b in the high half, both at bit pos(i).
+template <int BITS, int D>
+struct VCodes {
+    static constexpr int N = D / 8, NW = (N * BITS + 31) / 32;
+    __host__ __device__ static constexpr int pos(int i)
+    {
+        if (BITS == 4) return 4 * (i & 1);
+        constexpr int P[16] = {0, 3, 6, 1, 4, 7, 2, 5, 8, 3, 6, 1, 4, 7, 2, 5};
+        return P[i];
+    }
+    // the lane's codes of the row at `a`, from bit 0 of w[0]
+    __device__ __forceinline__ static void load(const uint8_t *a, int g, uint32_t (&w)[NW])
+    {
+        if constexpr (BITS == 4 && D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(a + 8 * g);
+            w[0] = v.x, w[1] = v.y;
+        } else if constexpr (BITS == 4) {
+            w[0] = lds32(a + 4 * g);
+        } else if constexpr (D == 128) {
+            const uint8_t *p = a + ((6 * g) & ~3);
+            const uint32_t s = 16 * (g & 1);
+            const uint32_t wa = lds32(p), wb = lds32(p + 4);
+            w[0] = __funnelshift_r(wa, wb, s);
+            w[1] = wb >> s;
+        } else {
+            const int o = 3 * g;  // 24 bits at byte 3g
+            const uint32_t wa = lds32(a + (o & ~3)), wb = lds32(a + ((o + 2) & ~3));
+            w[0] = __funnelshift_r(wa, wb, 8 * (o & 3));
+        }
+    }
+    __device__ __forceinline__ static void join(const uint32_t (&a)[NW], const uint32_t (&b)[NW], uint32_t (&x)[N])
+    {
+        if constexpr (BITS == 4) {
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j) {
+                const uint32_t m = prmt(a[j / 2], b[j / 2], (j & 1) ? 0x7632u : 0x5410u), u = m >> 8;
+                x[4 * j] = m & 0x000F000Fu;
+                x[4 * j + 1] = m & 0x00F000F0u;
+                x[4 * j + 2] = u & 0x000F000Fu;
+                x[4 * j + 3] = u & 0x00F000F0u;
+            }
+        } else {
+            const uint32_t b0 = prmt(a[0], b[0], 0x5410u), b1 = prmt(a[0], b[0], 0x6521u), b2 = prmt(a[0], b[0], 0x7632u);
+            x[0] = b0 & 0x00070007u;  // bits 0-15: codes 0, 1, 2
+            x[1] = b0 & 0x00380038u;
+            x[2] = b0 & 0x01C001C0u;
+            x[3] = b1 & 0x000E000Eu;  // bits 8-23: codes 3, 4, 5
+            x[4] = b1 & 0x00700070u;
+            x[5] = b1 & 0x03800380u;
+            x[6] = b2 & 0x001C001Cu;  // bits 16-31: codes 6, 7, 8
+            x[7] = b2 & 0x00E000E0u;
+            if constexpr (D == 128) {
+                x[8] = b2 & 0x07000700u;
+                const uint32_t b3 = prmt(__funnelshift_r(a[0], a[1], 24), __funnelshift_r(b[0], b[1], 24), 0x5410u);
+                x[9] = b3 & 0x00380038u;  // bits 24-39: codes 9, 10
+                x[10] = b3 & 0x01C001C0u;
+                const uint32_t b4 = prmt(a[1], b[1], 0x5410u), b5 = prmt(a[1], b[1], 0x6521u);
+                x[11] = b4 & 0x000E000Eu;  // bits 32-47: codes 11, 12, 13
+                x[12] = b4 & 0x00700070u;
+                x[13] = b4 & 0x03800380u;
+                x[14] = b5 & 0x001C001Cu;  // bits 40-55: codes 14, 15
+                x[15] = b5 & 0x00E000E0u;
+            }
+        }
+    }
+};
+
+// RT rows to a column tile of 8.  PREC: q' and w in two fp16 parts, and the codes multiplied up to normal fp16
+// numbers (a product with a subnormal keeps 10 bits less in the tensor core's sum: 6e-5 of the result, which is
+// nothing in bf16).  Columns: RT = 1: row 0's part t in column 2t, the odd ones empty (a lane then has half the
+// softmax to do); RT = 4: part * 4 + row; RT = 8 (one part): the rows.
+template <int BITS, int D, int RT, int NT, bool PREC>
+struct DecShape {
+    static constexpr int ROWS = NT * RT;
+    static constexpr int E = RT == 1 ? 1 : 2;  // columns of a lane that hold rows
+    static constexpr int RB = D * BITS / 8;    // bytes of a packed row
+    static constexpr uint32_t TILE = DEC_TILE * RB, STAGE = 2 * TILE;
+    static constexpr size_t RING = (size_t)DEC_WARPS * DEC_STAGES * STAGE;
+    static constexpr size_t JOIN = (size_t)DEC_WARPS * ROWS * (D + 2) * 4;  // the warps' results, when they are joined
+    static constexpr size_t SMEM = RING > JOIN ? RING : JOIN;
+    // row in the tile, and part, of column `col`
+    __device__ __forceinline__ static int row(int col) { return RT == 1 ? 0 : RT == 4 ? col & 3 : col; }
+    __device__ __forceinline__ static int part(int col) { return RT == 1 ? col >> 1 : RT == 4 ? col >> 2 : 0; }
+    __device__ __forceinline__ static bool used(int col) { return RT != 1 || (col & 1) == 0 && (col >> 1) < (PREC ? 2 : 1); }
+};
+
+template <int BITS, int D, int RT, int NT, bool PREC>
+__global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
+    paged_decode_kernel(const PagedAttnDev a)
+{
+    using S = DecShape<BITS, D, RT, NT, PREC>;
+    using KP = KPairs<BITS, D>;
+    using VC = VCodes<BITS, D>;
+    constexpr int E = S::E;
+    constexpr int XOR = RT == 1 ? 1 : 2;  // lane distance of a row's two parts
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[DEC_WARPS * DEC_STAGES];
+    __shared__ float s_sk[D], s_sv[D], s_zv[D];
+    __shared__ __align__(16) float s_q[S::ROWS * D];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
+    const Paged &p = a.p;
+    const int split = blockIdx.x % a.splits;
+    const int bh = blockIdx.x / a.splits, b = bh / a.H, h = bh % a.H;
+    int s0, n, L;
+    if (!paged_sequence(p, b, s0, n, L)) return;
+    const int rows = n * a.G;  // (token, head of the group), at most S::ROWS (the launcher's choice from max_q)
+    if (rows <= 0) return;
+    const int tiles = (L + DEC_TILE - 1) / DEC_TILE;
+    const int stride = a.splits * DEC_WARPS, first = split * DEC_WARPS + warp;
+    const int count = first < tiles ? (tiles - first - 1) / stride + 1 : 0;  // tiles of this warp
+
+    // ---- the warp's ring ----
+    const uint32_t ring = smem_u32(smem) + warp * DEC_STAGES * S::STAGE, bar0 = smem_u32(bars) + warp * DEC_STAGES * 8;
+    if (lane == 0) {
+        for (int s = 0; s < DEC_STAGES; ++s) mbar_init(bar0 + 8 * s, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    const bool small = p.shift == 4;  // pages of 16: a tile is two of them
+    const int last_page = (L - 1) >> p.shift;
+    int ids0 = 0, ids1 = 0;  // page ids of the 32 tiles from the last multiple of 32 on, one to a lane
+    auto issue = [&](int i) {  // the i-th tile of the warp, called for i = 0, 1, ... in order
+        if ((i & 31) == 0 && i + lane < count) {
+            const int pg = ((first + (i + lane) * stride) * DEC_TILE) >> p.shift;
+            ids0 = max(paged_page(p, b, pg), 0);
+            ids1 = small && pg + 1 <= last_page ? max(paged_page(p, b, pg + 1), 0) : -1;
+        }
+        const int id0 = __shfl_sync(FULL, ids0, i & 31);
+        const int id1 = small ? __shfl_sync(FULL, ids1, i & 31) : -1;
+        if (lane == 0) {
+            const int s = i % DEC_STAGES;
+            const uint32_t dst = ring + s * S::STAGE, bar = bar0 + 8 * s;
+            const int slot = ((first + i * stride) * DEC_TILE) & ((1 << p.shift) - 1);
+            const int64_t o0 = (paged_row(id0, a.H, h, p.shift) + slot) * S::RB;
+            const uint32_t bytes = small ? S::TILE / 2 : S::TILE;
+            mbar_expect_tx(bar, id1 >= 0 ? 4 * bytes : 2 * bytes);
+            bulk_g2s(dst, a.kq + o0, bytes, bar);
+            bulk_g2s(dst + S::TILE, a.vq + o0, bytes, bar);
+            if (id1 >= 0) {
+                const int64_t o1 = paged_row(id1, a.H, h, p.shift) * S::RB;
+                bulk_g2s(dst + bytes, a.kq + o1, bytes, bar);
+                bulk_g2s(dst + S::TILE + bytes, a.vq + o1, bytes, bar);
+            }
+        }
+    };
+    int issued = 0;
+    for (; issued < DEC_STAGES - 1 && issued < count; ++issued) issue(issued);
+
+    // ---- the head's channels, then the query fragments ----
+    for (int d = tid; d < D; d += DEC_THREADS) {
+        s_sk[d] = a.kt.sk[cluster_of(a.kt.ck, h * D + d, a.kt.g, p.err)];
+        const int kv = cluster_of(a.kt.cv, h * D + d, a.kt.g, p.err);
+        s_sv[d] = a.kt.sv[kv];
+        s_zv[d] = (float)a.kt.zv[kv];
+    }
+    __syncthreads();
+    // q' = q s of the rows, in fp32
+    for (int i = tid; i < S::ROWS * D; i += DEC_THREADS) {
+        const int r = i / D, d = i - r * D, tok = r / a.G, j = r - tok * a.G;
+        s_q[i] = r < rows ? load_elem(a.q, a.dtype, (int64_t)(s0 + tok) * a.q_stride + (int64_t)(h * a.G + j) * D + d) * s_sk[d] : 0.f;
+    }
+    __syncthreads();
+    // column gq of tile nt: the lane needs the channels of its quarter in the order of the K pairs
+    uint32_t qf[NT][KP::N];
+    float cx[NT][E];  // base-2 scores of the lane's columns = cx * S
+    int vis[NT][E];   // their visible positions (none in a column that holds no row)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const float *v = s_q + (nt * RT + S::row(gq)) * D + tq * (D / 4);
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; i += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(v + i);
+            m = fmaxf(fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+        }
+        m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
+        int ex = 0;
+        if (m > 0.f && m < INFINITY) frexpf(m, &ex);  // m < 2^ex
+        ex = max(ex, -100);
+        const float up = S::used(gq) ? ldexpf(1.f, 15 - ex) : 0.f;
+#pragma unroll
+        for (int i = 0; i < KP::N; ++i) {
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                w[e] = v[KP::code(i, e)] * up * (1.f / (float)(1 << KP::pos(i, e)));
+                if (PREC && S::part(gq) == 1) w[e] = fp16_rest(w[e]);
+            }
+            qf[nt][i] = half2_bits(w[0], w[1]);
+        }
+        const float c = ldexpf(a.scale * LOG2E, ex - 15 + (PREC ? 10 : 24));
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int col = 2 * tq + e, r = nt * RT + S::row(col);
+            cx[nt][e] = __shfl_sync(FULL, c, 4 * col);
+            vis[nt][e] = S::used(col) && r < rows ? L - n + r / a.G + 1 : 0;
+        }
+    }
+
+    float o[D / 16][NT][4];  // sums over the warp's positions: channels 2i, 2i + 1 of the lane's D / 8, two columns
+    float m[NT][E], off[NT][E], l[NT][E];  // reference of the exponents, DEC_PSHIFT - m, sum
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            m[nt][e] = -1e30f;
+            off[nt][e] = vis[nt][e] > 0 ? 1e30f : -INFINITY;
+            l[nt][e] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
+    }
+    // position of MMA row k (0-15) of a block: k with its low bits arranged so that the rows that the lanes of one
+    // shared-memory access read are neighbours, for K (rows gq) and for V (k = 2 tq, ...) alike
+    const int prow = gq ^ ((gq >> 1) & 1);
+    const int v0 = 2 * tq + (tq & 1), v1 = v0 ^ 1;
+    const bool rest = PREC && S::part(2 * tq) == 1;  // the lane's columns are second parts
+
+    bool ok = true;
+    for (int i = 0; i < count; ++i) {
+        if (issued < count) issue(issued++);
+        const int s = i % DEC_STAGES;
+        ok = __all_sync(FULL, mbar_wait_bounded(bar0 + 8 * s, (i / DEC_STAGES) & 1, p.err));
+        if (!ok) break;
+        const int pos0 = (first + i * stride) * DEC_TILE;
+        const uint8_t *kst = smem + (warp * DEC_STAGES + s) * S::STAGE, *vst = kst + S::TILE;
+        float x[2][NT][4];
+#pragma unroll
+        for (int bk = 0; bk < 2; ++bk) {
+            uint32_t ka[KP::N], kb[KP::N];
+            KP::load(kst + (16 * bk + prow) * S::RB, tq, ka);
+            KP::load(kst + (16 * bk + prow + 8) * S::RB, tq, kb);
+            if (PREC) {
+#pragma unroll
+                for (int j = 0; j < KP::N; ++j) ka[j] = code_up(ka[j]), kb[j] = code_up(kb[j]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[bk][nt][e] = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_16816(x[bk][nt], ka[2 * ks], kb[2 * ks], ka[2 * ks + 1], kb[2 * ks + 1], qf[nt][2 * ks],
+                              qf[nt][2 * ks + 1]);
+                if (PREC) {
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            x[bk][nt][2 * f + e] += __shfl_xor_sync(FULL, x[bk][nt][2 * f + e], XOR);
+                }
+            }
+        }
+        if (a.scores != nullptr && !rest) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int r = nt * RT + S::row(2 * tq + e);
+                    if (r >= rows || !S::used(2 * tq + e)) continue;
+                    const int tok = r / a.G, j = r - tok * a.G;
+                    float *dst = a.scores + ((int64_t)(s0 + tok) * a.Hq + h * a.G + j) * p.max_len;
+#pragma unroll
+                    for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const int pos = pos0 + 16 * bk + prow + 8 * f;
+                            if (pos < L) dst[pos] = x[bk][nt][2 * f + e] * cx[nt][e];
+                        }
+                }
+        }
+        // exponents against the reference m: y = x - m + DEC_PSHIFT, -inf where the row does not see the position.
+        // m only has to keep 2^y inside fp16; it moves when some y passes DEC_YMAX, seldom after the first tile.
+        const bool whole = pos0 + DEC_TILE <= L - n + 1;  // every row sees the whole tile
+        auto exponent = [&](int bk, int nt, int f, int e) {
+            const float v = fmaf(x[bk][nt][2 * f + e], cx[nt][e], off[nt][e]);
+            return whole || pos0 + 16 * bk + prow + 8 * f < vis[nt][e] ? v : -INFINITY;
+        };
+        float y[2][NT][2][E];
+        bool over = false;
+#pragma unroll
+        for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        y[bk][nt][f][e] = exponent(bk, nt, f, e);
+                        over |= y[bk][nt][f][e] > DEC_YMAX;
+                    }
+        if (__any_sync(FULL, over)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    float mn = m[nt][e];
+#pragma unroll
+                    for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f)
+                            if (pos0 + 16 * bk + prow + 8 * f < vis[nt][e]) mn = fmaxf(mn, x[bk][nt][2 * f + e] * cx[nt][e]);
+#pragma unroll
+                    for (int f = 4; f < 32; f <<= 1) mn = fmaxf(mn, __shfl_xor_sync(FULL, mn, f));
+                    if (vis[nt][e] > 0 && mn > -1e30f) {
+                        const float r = ex2(m[nt][e] - mn);
+                        m[nt][e] = mn;
+                        off[nt][e] = (float)DEC_PSHIFT - mn;
+                        l[nt][e] *= r;
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            o[c][nt][e] *= r;
+                            o[c][nt][2 + e] *= r;
+                        }
+                    }
+#pragma unroll
+                    for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) y[bk][nt][f][e] = exponent(bk, nt, f, e);
+                }
+        }
+        // weights, then O += V^T w^T block by block
+#pragma unroll
+        for (int bk = 0; bk < 2; ++bk) {
+            uint32_t w[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    float pv[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < E; ++e) pv[e] = ex2(y[bk][nt][f][e]);
+                    uint32_t hw = half2_bits(pv[0], pv[1]);
+                    const float2 r2 = __half22float2(*reinterpret_cast<const __half2 *>(&hw));
+                    if (PREC) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) l[nt][e] += pv[e];
+                        const uint32_t lw = half2_bits(pv[0] - r2.x, pv[1] - r2.y);
+                        hw = rest ? lw : hw;
+                    } else {  // the rounded weights are summed: numerator and denominator hold the same ones
+                        l[nt][0] += r2.x;
+                        if (E == 2) l[nt][E - 1] += r2.y;
+                    }
+                    w[nt][f] = mat_trans(hw);
+                }
+            uint32_t ra[VC::NW], rc[VC::NW], xa[VC::N], xb[VC::N];
+            VC::load(vst + (16 * bk + v0) * S::RB, gq, ra);
+            VC::load(vst + (16 * bk + v1) * S::RB, gq, rc);
+            VC::join(ra, rc, xa);
+            VC::load(vst + (16 * bk + v0 + 8) * S::RB, gq, ra);
+            VC::load(vst + (16 * bk + v1 + 8) * S::RB, gq, rc);
+            VC::join(ra, rc, xb);
+            if (PREC) {
+#pragma unroll
+                for (int j = 0; j < VC::N; ++j) xa[j] = code_up(xa[j]), xb[j] = code_up(xb[j]);
+            }
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_16816(o[c][nt], xa[2 * c], xa[2 * c + 1], xb[2 * c], xb[2 * c + 1], w[nt][0], w[nt][1]);
+        }
+        __syncwarp();  // the stage has been read (its values went into the MMAs above)
+    }
+    if (!ok)  // a wait ran out: no copy may be in flight into this CTA's memory when it ends
+        for (int i = max(0, issued - DEC_STAGES); i < issued; ++i)
+            mbar_wait_bounded(bar0 + 8 * (i % DEC_STAGES), (i / DEC_STAGES) & 1, p.err);
+
+    // ---- join the warps ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int f = 4; f < 32; f <<= 1) l[nt][e] += __shfl_xor_sync(FULL, l[nt][e], f);
+    __syncthreads();  // every warp is done with its ring
+    float *js = reinterpret_cast<float *>(smem);            // [warp][row][D]
+    float *jm = js + DEC_WARPS * S::ROWS * D;               // [warp][row]
+    float *jl = jm + DEC_WARPS * S::ROWS;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int r = nt * RT + S::row(2 * tq + e);
+            const bool mine = S::used(2 * tq + e) && !rest;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    float v = o[c][nt][2 * f + e];
+                    if (PREC) v += __shfl_xor_sync(FULL, v, XOR);
+                    // the codes' power of two and the weights' 2^DEC_PSHIFT
+                    v *= (float)(1 << ((PREC ? 10 : 24) - VC::pos(2 * c + f))) * (1.f / (float)(1 << DEC_PSHIFT));
+                    if (mine) js[(warp * S::ROWS + r) * D + gq * (D / 8) + 2 * c + f] = v;
+                }
+            if (gq == 0 && mine) {
+                jm[warp * S::ROWS + r] = l[nt][e] == 0.f ? -INFINITY : m[nt][e];
+                jl[warp * S::ROWS + r] = l[nt][e] * (1.f / (float)(1 << DEC_PSHIFT));
+            }
+        }
+    __syncthreads();
+    for (int i = tid; i < rows * D; i += DEC_THREADS) {
+        const int r = i / D, d = i - r * D;
+        const int tok = r / a.G, j = r - tok * a.G;
+        const int64_t row = (int64_t)(s0 + tok) * a.Hq + h * a.G + j;
+        float mt = -INFINITY, lt = 0.f, v = 0.f;
+#pragma unroll
+        for (int w = 0; w < DEC_WARPS; ++w) mt = fmaxf(mt, jm[w * S::ROWS + r]);
+#pragma unroll
+        for (int w = 0; w < DEC_WARPS; ++w) {
+            const float mw = jm[w * S::ROWS + r];
+            const float f = mw == -INFINITY ? 0.f : ex2(mw - mt);
+            lt = fmaf(jl[w * S::ROWS + r], f, lt);
+            v = fmaf(js[(w * S::ROWS + r) * D + d], f, v);
+        }
+        if (a.part == nullptr) {
+            const bool sees = mt != -INFINITY;
+            store_elem(a.out, a.dtype, row * D + d, sees ? s_sv[d] * (v / lt - s_zv[d]) : 0.f);
+        } else {
+            a.part[((int64_t)split * p.T * a.Hq + row) * D + d] = v;
+            if (d == 0) {
+                float *ml = a.ml + ((int64_t)split * p.T * a.Hq + row) * 2;
+                ml[0] = mt;
+                ml[1] = lt;
+            }
+        }
+    }
+}
+
+// Joins the parts of every row (the first T Hq CTAs, one to a row), and adds the weights (the others, one to a
+// block of CMB_KEYS positions of a (sequence, K/V head)).
+constexpr int CMB_THREADS = 128, CMB_KEYS = 512;
+
+// Base-2 maximum and sum of a row over its parts, by one warp: every lane gets them.
+__device__ __forceinline__ void join_parts(const float *ml, int64_t R, int64_t row, int splits, float &mt, float &lt)
+{
+    const int lane = threadIdx.x & 31;
+    mt = -INFINITY;
+    lt = 0.f;
+    for (int s = lane; s < splits; s += 32) mt = fmaxf(mt, ml[(s * R + row) * 2]);
+    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, o));
+    if (mt == -INFINITY) return;
+    for (int s = lane; s < splits; s += 32) lt += ml[(s * R + row) * 2 + 1] * ex2(ml[(s * R + row) * 2] - mt);
+    for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(FULL, lt, o);
+}
+
+template <int D>
+__global__ void __launch_bounds__(CMB_THREADS)
+    paged_combine_kernel(const PagedAttnDev a, int blocks)
+{
+    extern __shared__ float s_f[];  // a factor per part, or per row the base-2 log of the sum
+    const Paged &p = a.p;
+    const int tid = threadIdx.x;
+    const int64_t R = p.T * a.Hq;
+    if (blockIdx.x < R) {
+        const int64_t row = blockIdx.x, t = row / a.Hq;
+        const int b = paged_row_sequence(p, t);
+        int s0, n, L;
+        if (b < 0 || !paged_sequence(p, b, s0, n, L)) return;
+        float mt, lt;
+        join_parts(a.ml, R, row, a.splits, mt, lt);
+        for (int s = tid; s < a.splits; s += CMB_THREADS) {
+            const float ms = a.ml[(s * R + row) * 2];
+            s_f[s] = ms == -INFINITY ? 0.f : ex2(ms - mt) / lt;
+        }
+        __syncthreads();
+        const int h = (int)(row % a.Hq) / a.G;
+        for (int d = tid; d < D; d += CMB_THREADS) {
+            float v = 0.f;
+#pragma unroll 8
+            for (int s = 0; s < a.splits; ++s) v = fmaf(a.part[(s * R + row) * D + d], s_f[s], v);
+            const int k = cluster_of(a.kt.cv, h * D + d, a.kt.g, p.err);
+            store_elem(a.out, a.dtype, row * D + d, mt == -INFINITY ? 0.f : a.kt.sv[k] * (v - (float)a.kt.zv[k]));
+        }
+        return;
+    }
+    const int64_t u = blockIdx.x - R;
+    const int blk = (int)(u % blocks), bh = (int)(u / blocks), b = bh / a.H, h = bh % a.H;
+    int s0, n, L;
+    if (!paged_sequence(p, b, s0, n, L)) return;
+    const int rows = n * a.G;
+    if (rows == 0 || blk * CMB_KEYS >= L) return;
+    auto row_of = [&](int r) { return (int64_t)(s0 + r / a.G) * a.Hq + h * a.G + r % a.G; };
+    for (int r = tid >> 5; r < rows; r += CMB_THREADS / 32) {
+        float mt, lt;
+        join_parts(a.ml, R, row_of(r), a.splits, mt, lt);
+        if ((tid & 31) == 0) s_f[r] = mt == -INFINITY ? INFINITY : mt + log2f(lt);
+    }
+    __syncthreads();
+    for (int pos = blk * CMB_KEYS + tid; pos < min(L, (blk + 1) * CMB_KEYS); pos += CMB_THREADS) {
+        float w = 0.f;
+        for (int r = 0; r < rows; ++r)
+            if (pos <= L - n + r / a.G) w += ex2(a.scores[row_of(r) * p.max_len + pos] - s_f[r]);
+        const int page = paged_page(p, b, pos >> p.shift);
+        if (page >= 0) a.weights[paged_row(page, a.H, h, p.shift) + (pos & ((1 << p.shift) - 1))] += w;
+    }
+}
+
+// ---- launch ----------------------------------------------------------------------------------------------
+namespace {
+struct DecPlan {
+    bool prec;
+    int rt, nt, splits;
+};
+constexpr int DEC_MAX_SPLITS = 64;
+DecPlan dec_plan(int Hq, int H, int dtype, int B, int max_q, int max_len, int weights, int num_sms)
+{
+    DecPlan pl;
+    const int64_t rows = (int64_t)max_q * (Hq / H);
+    pl.prec = weights || dtype != RPTQ_BF16;  // fp16's and fp32's results, and the sums, are finer than one part
+    pl.rt = rows == 1 ? 1 : pl.prec ? 4 : 8;
+    pl.nt = rows <= pl.rt ? 1 : rows <= 2 * pl.rt ? 2 : 4;
+    // parts: enough for three CTAs to an SM, each warp at least two tiles
+    const int64_t units = (int64_t)B * H;
+    const int64_t want = (PERSM * num_sms + units - 1) / units, tiles = (max_len + DEC_TILE - 1) / DEC_TILE;
+    pl.splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles / (2 * DEC_WARPS), DEC_MAX_SPLITS}));
+    return pl;
+}
+}  // namespace
+
+// at most 16 rows in two parts, 32 in one
+bool paged_decode_takes(int Hq, int H, int D, int dtype, int max_q, int weights)
+{
+    if (D != 64 && D != 128) return false;
+    const int64_t rows = (int64_t)max_q * (Hq / H);
+    return rows <= (weights || dtype != RPTQ_BF16 ? 16 : 32);
+}
+
+size_t paged_decode_workspace(int64_t T, int Hq, int H, int D, int dtype, int B, int max_q, int max_len, int weights,
+                              int num_sms)
+{
+    const DecPlan pl = dec_plan(Hq, H, dtype, B, max_q, max_len, weights, num_sms);
+    size_t bytes = 0;
+    if (pl.splits > 1 || weights) bytes += (size_t)pl.splits * T * Hq * (D + 2) * 4;
+    if (weights) bytes += (size_t)T * Hq * max_len * 4;
+    return bytes;
+}
+
+template <int BITS, int D, int RT, int NT, bool PREC>
+static cudaError_t launch_dec(const PagedAttnDev &d, const DecPlan &pl, int B, cudaStream_t stream)
+{
+    using S = DecShape<BITS, D, RT, NT, PREC>;
+    auto kern = paged_decode_kernel<BITS, D, RT, NT, PREC>;
+    cudaError_t e = kernel_smem((const void *)kern, S::SMEM);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)((int64_t)B * d.H * pl.splits), DEC_THREADS, S::SMEM, stream>>>(d);
+    return cudaGetLastError();
+}
+template <int BITS, int D>
+static cudaError_t launch_dec_rows(const PagedAttnDev &d, const DecPlan &pl, int B, cudaStream_t stream)
+{
+    if (pl.rt == 1)
+        return pl.prec ? launch_dec<BITS, D, 1, 1, true>(d, pl, B, stream) : launch_dec<BITS, D, 1, 1, false>(d, pl, B, stream);
+    if (pl.prec)
+        return pl.nt == 1   ? launch_dec<BITS, D, 4, 1, true>(d, pl, B, stream)
+               : pl.nt == 2 ? launch_dec<BITS, D, 4, 2, true>(d, pl, B, stream)
+                            : launch_dec<BITS, D, 4, 4, true>(d, pl, B, stream);
+    return pl.nt == 1   ? launch_dec<BITS, D, 8, 1, false>(d, pl, B, stream)
+           : pl.nt == 2 ? launch_dec<BITS, D, 8, 2, false>(d, pl, B, stream)
+                        : launch_dec<BITS, D, 8, 4, false>(d, pl, B, stream);
+}
+
+cudaError_t launch_paged_decode(const PagedAttnArgs &a)
+{
+    const DecPlan pl = dec_plan(a.Hq, a.H, a.dtype, a.B, a.max_q, a.max_len, a.weights != nullptr, a.num_sms);
+    PagedAttnDev d{};
+    d.p = Paged{a.start, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, a.max_q, a.max_len, a.err};
+    d.q = a.q, d.out = a.out, d.dtype = a.dtype, d.Hq = a.Hq, d.H = a.H, d.G = a.Hq / a.H, d.q_stride = a.q_stride;
+    d.kq = a.kq, d.vq = a.vq, d.kt = a.kt, d.scale = a.scale, d.weights = a.weights, d.splits = pl.splits;
+    const bool join = pl.splits > 1 || a.weights;
+    if (join) {
+        d.part = static_cast<float *>(a.ws);
+        d.ml = d.part + (int64_t)pl.splits * a.T * a.Hq * a.D;
+        if (a.weights) d.scores = d.ml + (int64_t)pl.splits * a.T * a.Hq * 2;
+    }
+    cudaError_t e = a.bits == 4 ? (a.D == 128 ? launch_dec_rows<4, 128>(d, pl, a.B, a.stream) : launch_dec_rows<4, 64>(d, pl, a.B, a.stream))
+                                : (a.D == 128 ? launch_dec_rows<3, 128>(d, pl, a.B, a.stream) : launch_dec_rows<3, 64>(d, pl, a.B, a.stream));
+    if (e != cudaSuccess || !join) return e;
+    const int blocks = a.weights ? std::max(1, (a.max_len + CMB_KEYS - 1) / CMB_KEYS) : 0;
+    const unsigned grid = (unsigned)(a.T * a.Hq + (int64_t)a.B * a.H * blocks);
+    const size_t smem = std::max<size_t>(pl.splits, (size_t)a.max_q * d.G) * 4;
+    if (a.D == 128)
+        paged_combine_kernel<128><<<grid, CMB_THREADS, smem, a.stream>>>(d, blocks);
+    else
+        paged_combine_kernel<64><<<grid, CMB_THREADS, smem, a.stream>>>(d, blocks);
+    return cudaGetLastError();
+}
+
+}  // namespace rptq

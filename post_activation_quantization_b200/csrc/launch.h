@@ -323,7 +323,8 @@ cudaError_t launch_paged_append(const PagedAppendArgs &a);
 cudaError_t launch_paged_dequant(const PagedDequantArgs &a);
 cudaError_t launch_paged_evict(const PagedEvictArgs &a);
 cudaError_t launch_paged_attention(const PagedAttnArgs &a);
-size_t paged_attention_workspace(int64_t T, int Hq, int weights);
+size_t paged_attention_workspace(int64_t T, int Hq, int H, int D, int dtype, int B, int max_q, int max_len, int weights,
+                                 int num_sms);
 cudaError_t launch_linear_prepare(const LinPrepArgs &a);
 cudaError_t launch_reordered_linear(const LinArgs &a);
 // largest number of cache positions one decode-attention call reads (its scores stay in shared

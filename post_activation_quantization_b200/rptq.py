@@ -387,18 +387,22 @@ def _need(ok, where: str):
         raise RptqError(RPTQ_ERR_INVALID_ARG, where)
 
 
-def _arg(t: torch.Tensor | None, dtype, shape, dev, where: str, rows: bool = False):
-    """Address of a tensor that must have this type, shape (None: any) and device; contiguous, or
-    (rows) [T, heads, D] whose rows may be further apart than one row."""
+def _arg(t: torch.Tensor | None, dtype, shape, dev: int, where: str):
+    """Address of a contiguous tensor that must have this type, shape and device index."""
     if t is None:
         return None
-    ok = t.dtype == dtype and t.device == dev and t.dim() == len(shape) and all(
-        s is None or s == x for s, x in zip(shape, t.shape))
-    if rows:
-        ok = ok and (t.numel() == 0 or (t.stride(2) == 1 and t.stride(1) == t.shape[2]))
-    else:
-        ok = ok and t.is_contiguous()
-    _need(ok, where)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise RptqError(RPTQ_ERR_INVALID_ARG, where)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor | None, dtype, shape, dev: int, where: str):
+    """Address of a [T, heads, D] tensor whose rows may be further apart than one row."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not (
+            t.numel() == 0 or (t.stride(2) == 1 and t.stride(1) == shape[2])):
+        raise RptqError(RPTQ_ERR_INVALID_ARG, where)
     return t.data_ptr()
 
 
@@ -407,20 +411,27 @@ def _row_stride(t: torch.Tensor) -> int:
 
 
 def _paged(pages: torch.Tensor, page_table: torch.Tensor, bits: int, where: str):
-    """(device, H, D, B, max_pages, n_pages, page_size) of a pool and its page table."""
-    _need(pages.dim() == 4 and page_table.dim() == 2 and pages.is_cuda, where)
-    dev = pages.device
-    _need(dev.index == torch.cuda.current_device(), where)
+    """(device index, H, D, B, max_pages, n_pages, page_size) of a pool and its page table."""
+    dev = pages.get_device()
+    _need(pages.dim() == 4 and page_table.dim() == 2 and dev >= 0 and dev == torch._C._cuda_getDevice(), where)
     n_pages, H, P, rb = pages.shape
     _need(bits > 0 and rb * 8 % bits == 0, where)
-    return dev, H, rb * 8 // bits, page_table.shape[0], page_table.shape[1], n_pages, P
+    B, max_pages = page_table.shape
+    return dev, H, rb * 8 // bits, B, max_pages, n_pages, P
 
 
-def _clusters(cluster, scale, zero, C: int, dev, where: str):
+def _clusters(cluster, scale, zero, C: int, dev: int, where: str):
     """Addresses of one tensor's (cluster, scale, zero) and its cluster count."""
     g = scale.numel()
     return (_arg(cluster, torch.int32, (C,), dev, where), _arg(scale, torch.float32, (g,), dev, where),
             _arg(zero, torch.int32, (g,), dev, where)), g
+
+
+def _stream_handle(stream) -> int:
+    """The raw handle of a stream (the current stream of the current device without one)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def rptq_kv_paged_append(k_new, v_new, start, lens, page_table, k_pages, v_pages, cluster_k, scale_k, zero_k, cluster_v,
@@ -444,12 +455,12 @@ def rptq_kv_paged_append(k_new, v_new, start, lens, page_table, k_pages, v_pages
     if k_new is not None and v_new is not None:
         _need(T < 2 or k_new.stride(0) == v_new.stride(0), w)
     st = lib().rptq_kv_paged_append(
-        _arg(k_new, x.dtype, (T, H, D), dev, w, True), _arg(v_new, x.dtype, (T, H, D), dev, w, True), _DT[x.dtype], T, H, D,
+        _rows(k_new, x.dtype, (T, H, D), dev, w), _rows(v_new, x.dtype, (T, H, D), dev, w), _DT[x.dtype], T, H, D,
         _row_stride(x), _arg(start, torch.int32, (B + 1,), dev, w), _arg(lens, torch.int32, (B,), dev, w), B,
         _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages, P, *ck, *cv, g.pop(), bits,
         _arg(k_pages, torch.uint8, pool.shape, dev, w) if k_new is not None else None,
         _arg(v_pages, torch.uint8, pool.shape, dev, w) if v_new is not None else None,
-        _arg(weights, torch.float32, (n_pages, H, P), dev, w), _stream(stream))
+        _arg(weights, torch.float32, (n_pages, H, P), dev, w), _stream_handle(stream))
     _check(st, w)
     return k_pages, v_pages
 
@@ -462,14 +473,14 @@ def rptq_kv_paged_dequant(pages, page_table, start, begin, cluster, scale, zero,
     dev, H, D, B, max_pages, n_pages, P = _paged(pages, page_table, bits, w)
     if out is None:
         _need(T is not None, w)
-        out = torch.empty((T, H, D), dtype=out_dtype, device=dev)
+        out = torch.empty((T, H, D), dtype=out_dtype, device=pages.device)
     _need(out.dtype in _DT, w)
     cl, g = _clusters(cluster, scale, zero, H * D, dev, w)
     T = out.shape[0]
     st = lib().rptq_kv_paged_dequant(
         _arg(pages, torch.uint8, pages.shape, dev, w), H, D, bits, _arg(start, torch.int32, (B + 1,), dev, w),
         _arg(begin, torch.int32, (B,), dev, w), B, _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages,
-        P, T, *cl, g, _arg(out, out.dtype, (T, H, D), dev, w), _DT[out.dtype], _stream(stream))
+        P, T, *cl, g, _arg(out, out.dtype, (T, H, D), dev, w), _DT[out.dtype], _stream_handle(stream))
     _check(st, w)
     return out
 
@@ -491,24 +502,24 @@ def rptq_kv_paged_attention(q, start, lens, page_table, k_pages, v_pages, cluste
     T, Hq, _ = q.shape
     dt = _DT[q.dtype]
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
     L = lib()
     ws_bytes = L.rptq_kv_paged_attention_workspace_size(T, Hq, H, D, dt, B, max_q, max_len, weights is not None)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
     elif workspace.numel() * workspace.element_size() < ws_bytes:
         raise RptqError(RPTQ_ERR_WORKSPACE, w)
     ck, g = _clusters(cluster_k, scale_k, zero_k, H * D, dev, w)
     cv, gv = _clusters(cluster_v, scale_v, zero_v, H * D, dev, w)
     _need(g == gv, w)
     st = L.rptq_kv_paged_attention(
-        _arg(q, q.dtype, (T, Hq, D), dev, w, True), dt, T, Hq, H, D, _row_stride(q),
+        _rows(q, q.dtype, (T, Hq, D), dev, w), dt, T, Hq, H, D, _row_stride(q),
         _arg(start, torch.int32, (B + 1,), dev, w), _arg(lens, torch.int32, (B,), dev, w), B, max_q, max_len,
         _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages, P,
         _arg(k_pages, torch.uint8, k_pages.shape, dev, w), _arg(v_pages, torch.uint8, k_pages.shape, dev, w), *ck, *cv, g, bits,
         float(scale), _arg(out, q.dtype, (T, Hq, D), dev, w), _arg(weights, torch.float32, (n_pages, H, P), dev, w),
         None if workspace is None else _arg(workspace, workspace.dtype, workspace.shape, dev, w),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check(st, w)
     return out
 
@@ -520,15 +531,15 @@ def rptq_kv_paged_evict(k_pages, v_pages, weights, lens, page_table, bits: int, 
     w = "rptq_kv_paged_evict"
     dev, H, D, B, max_pages, n_pages, P = _paged(k_pages, page_table, bits, w)
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        new_lens = torch.empty(B, dtype=torch.int32, device=lens.device)
     if kept is None:
-        kept = torch.empty((B, H, max(budget, 0)), dtype=torch.int32, device=dev)
+        kept = torch.empty((B, H, max(budget, 0)), dtype=torch.int32, device=lens.device)
     st = lib().rptq_kv_paged_evict(
         _arg(k_pages, torch.uint8, k_pages.shape, dev, w), _arg(v_pages, torch.uint8, k_pages.shape, dev, w),
         _arg(weights, torch.float32, (n_pages, H, P), dev, w), B, H, D, bits, _arg(lens, torch.int32, (B,), dev, w),
         _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages, P,
         max_pages * P if max_len is None else max_len, budget, recent, _arg(new_lens, torch.int32, (B,), dev, w),
-        _arg(kept, torch.int32, (B, H, max(budget, 0)), dev, w), _stream(stream))
+        _arg(kept, torch.int32, (B, H, max(budget, 0)), dev, w), _stream_handle(stream))
     _check(st, w)
     return new_lens, kept
 
