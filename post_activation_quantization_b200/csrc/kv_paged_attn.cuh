@@ -86,6 +86,7 @@ struct PagedAttnDev {
     // sum) [splits, T Hq, 2], and (with weights) the scores [T Hq, max_len], all base 2
     int splits;
     float *part, *ml, *scores;
+    float mid;  // what the codes of V have had taken off in `part`
 };
 
 // few rows to a K/V head (kv_paged_decode.cu)

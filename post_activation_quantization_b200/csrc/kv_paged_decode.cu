@@ -58,6 +58,16 @@ __device__ __forceinline__ uint32_t code_up(uint32_t v)
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x74007400u));
     return r;
 }
+// the same less 2^14 * mid * 2^(pos - 24): two codes about their middle
+template <int POS, int MID>
+__device__ __forceinline__ uint32_t code_about_mid(uint32_t v)
+{
+    constexpr int LOG = MID == 8 ? 3 : 2;  // MID * 2^(POS - 10) is a power of two
+    constexpr uint32_t H = 0x8000u | (uint32_t)(POS + LOG - 10 + 15) << 10;
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x74007400u), "r"(H | H << 16));
+    return r;
+}
 __device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
 // ---- K: one thread's D / 4 consecutive codes of a row as D / 8 pairs --------------------------------------
@@ -138,7 +148,16 @@ struct KPairs {
 // x[i] holds code i of row a in the low half and of row b in the high half, both at bit pos(i).
 template <int BITS, int D>
 struct VCodes {
-    static constexpr int N = D / 8, NW = (N * BITS + 31) / 32;
+    static constexpr int N = D / 8, NW = (N * BITS + 31) / 32, MID = 1 << (BITS - 1);
+    // the codes about their middle, so that the sums over positions stay small where the values cancel
+    template <int I = 0>
+    __device__ __forceinline__ static void about_mid(uint32_t (&x)[N])
+    {
+        if constexpr (I < N) {
+            x[I] = code_about_mid<pos(I), MID>(x[I]);
+            about_mid<I + 1>(x);
+        }
+    }
     __host__ __device__ static constexpr int pos(int i)
     {
         if (BITS == 4) return 4 * (i & 1);
@@ -202,11 +221,16 @@ struct VCodes {
     }
 };
 
-// RT rows to a column tile of 8.  PREC: q' and w in two fp16 parts, and the codes multiplied up to normal fp16
-// numbers (a product with a subnormal keeps 10 bits less in the tensor core's sum: 6e-5 of the result, which is
-// nothing in bf16).  Columns: RT = 1: row 0's part t in column 2t, the odd ones empty (a lane then has half the
-// softmax to do); RT = 4: part * 4 + row; RT = 8 (one part): the rows.
-template <int BITS, int D, int RT, int NT, bool PREC>
+// RT rows to a column tile of 8.  PREC says what the result must be good to:
+//   0 (bf16): q' one fp16, the codes as they are.  A product with a subnormal keeps 10 bits less in the tensor
+//     core's sum (6e-5 of it), which is nothing in bf16.
+//   1 (fp16, or running sums kept): q' in PARTS parts of 11 bits on one fixed grid -- with the codes multiplied up to
+//     normal fp16 numbers every product and every sum of a part is exact -- so that a score has fp32's rounding and no
+//     other; the weights one fp16.
+//   2 (fp32): the same, V's codes multiplied up too and the weights in two fp16 parts.
+// Columns: RT = 1: row 0's part t in column 2t, the odd ones empty (a lane then has half the softmax to do);
+// RT = 4: part * 4 + row; RT = 8 (one part): the rows.
+template <int BITS, int D, int RT, int NT, int PREC>
 struct DecShape {
     static constexpr int ROWS = NT * RT;
     static constexpr int E = RT == 1 ? 1 : 2;  // columns of a lane that hold rows
@@ -215,13 +239,14 @@ struct DecShape {
     static constexpr size_t RING = (size_t)DEC_WARPS * DEC_STAGES * STAGE;
     static constexpr size_t JOIN = (size_t)DEC_WARPS * ROWS * (D + 2) * 4;  // the warps' results, when they are joined
     static constexpr size_t SMEM = RING > JOIN ? RING : JOIN;
+    static constexpr int PARTS = PREC == 0 ? 1 : RT == 1 ? 3 : 2;  // of q'
     // row in the tile, and part, of column `col`
     __device__ __forceinline__ static int row(int col) { return RT == 1 ? 0 : RT == 4 ? col & 3 : col; }
     __device__ __forceinline__ static int part(int col) { return RT == 1 ? col >> 1 : RT == 4 ? col >> 2 : 0; }
-    __device__ __forceinline__ static bool used(int col) { return RT != 1 || (col & 1) == 0 && (col >> 1) < (PREC ? 2 : 1); }
+    __device__ __forceinline__ static bool used(int col) { return RT != 1 || ((col & 1) == 0 && (col >> 1) < PARTS); }
 };
 
-template <int BITS, int D, int RT, int NT, bool PREC>
+template <int BITS, int D, int RT, int NT, int PREC>
 __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
     paged_decode_kernel(const PagedAttnDev a)
 {
@@ -234,6 +259,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
     __shared__ __align__(8) uint64_t bars[DEC_WARPS * DEC_STAGES];
     __shared__ float s_sk[D], s_sv[D], s_zv[D];
     __shared__ __align__(16) float s_q[S::ROWS * D];
+    __shared__ __align__(16) uint8_t s_ref[S::RB];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
     const Paged &p = a.p;
     const int split = blockIdx.x % a.splits;
@@ -288,7 +314,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
         s_sk[d] = a.kt.sk[cluster_of(a.kt.ck, h * D + d, a.kt.g, p.err)];
         const int kv = cluster_of(a.kt.cv, h * D + d, a.kt.g, p.err);
         s_sv[d] = a.kt.sv[kv];
-        s_zv[d] = (float)a.kt.zv[kv];
+        s_zv[d] = (float)a.kt.zv[kv] - (PREC == 2 ? VC::MID : 0);
     }
     __syncthreads();
     // q' = q s of the rows, in fp32
@@ -315,23 +341,59 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
         int ex = 0;
         if (m > 0.f && m < INFINITY) frexpf(m, &ex);  // m < 2^ex
         ex = max(ex, -100);
-        const float up = S::used(gq) ? ldexpf(1.f, 15 - ex) : 0.f;
+        const int grid = PREC ? 11 : 15;  // largest |q'| in [2^(grid - 1), 2^grid)
+        const float up = S::used(gq) ? ldexpf(1.f, grid - ex) : 0.f;
 #pragma unroll
         for (int i = 0; i < KP::N; ++i) {
             float w[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                w[e] = v[KP::code(i, e)] * up * (1.f / (float)(1 << KP::pos(i, e)));
-                if (PREC && S::part(gq) == 1) w[e] = fp16_rest(w[e]);
+                float f = v[KP::code(i, e)] * up;
+                if (PREC) {  // part j: the integer nearest to what the parts before it leave, times 2^(11 j)
+                    float g = rintf(f);
+#pragma unroll
+                    for (int j = 1; j < S::PARTS; ++j)
+                        if (j <= S::part(gq)) {
+                            f = (f - g) * 2048.f;
+                            g = rintf(f);
+                        }
+                    f = g;
+                }
+                w[e] = f * (1.f / (float)(1 << KP::pos(i, e)));
             }
             qf[nt][i] = half2_bits(w[0], w[1]);
         }
-        const float c = ldexpf(a.scale * LOG2E, ex - 15 + (PREC ? 10 : 24));
+        const float c = ldexpf(a.scale * LOG2E, ex - grid + (PREC ? 10 : 24));
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int col = 2 * tq + e, r = nt * RT + S::row(col);
             cx[nt][e] = __shfl_sync(FULL, c, 4 * col);
             vis[nt][e] = S::used(col) && r < rows ? L - n + r / a.G + 1 : 0;
+        }
+    }
+
+    // Scores are taken relative to position 0's, subtracted in the (exact) sums of each part: what is left has the size
+    // of the scores' spread, while q' code alone carries the channels' means times q.
+    float xr[NT][4];  // [2] and [3] equal [0] and [1]
+    {
+        if (L > 0)
+            for (int i = tid; i < S::RB / 4; i += DEC_THREADS)
+                reinterpret_cast<uint32_t *>(s_ref)[i] =
+                    __ldg(reinterpret_cast<const uint32_t *>(a.kq + paged_row(max(paged_page(p, b, 0), 0), a.H, h, p.shift) * S::RB) + i);
+        __syncthreads();
+        uint32_t kr[KP::N];
+        KP::load(s_ref, tq, kr);
+        if (PREC) {
+#pragma unroll
+            for (int j = 0; j < KP::N; ++j) kr[j] = code_up(kr[j]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) xr[nt][e] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_16816(xr[nt], kr[2 * ks], kr[2 * ks], kr[2 * ks + 1], kr[2 * ks + 1], qf[nt][2 * ks], qf[nt][2 * ks + 1]);
         }
     }
 
@@ -354,7 +416,9 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
     // shared-memory access read are neighbours, for K (rows gq) and for V (k = 2 tq, ...) alike
     const int prow = gq ^ ((gq >> 1) & 1);
     const int v0 = 2 * tq + (tq & 1), v1 = v0 ^ 1;
-    const bool rest = PREC && S::part(2 * tq) == 1;  // the lane's columns are second parts
+    const int part = S::part(2 * tq);  // of the lane's columns
+    const bool head = part == 0;       // the lane's columns are the rows' first (or only) parts
+    const float part_scale = part == 0 ? 1.f : part == 1 ? 0x1p-11f : part == 2 ? 0x1p-22f : 0.f;
 
     bool ok = true;
     for (int i = 0; i < count; ++i) {
@@ -377,21 +441,25 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[bk][nt][e] = 0.f;
+                for (int e = 0; e < 4; ++e) x[bk][nt][e] = -xr[nt][e];
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     mma_16816(x[bk][nt], ka[2 * ks], kb[2 * ks], ka[2 * ks + 1], kb[2 * ks + 1], qf[nt][2 * ks],
                               qf[nt][2 * ks + 1]);
-                if (PREC) {
+                if (PREC) {  // the parts' sum, in every lane of the row
 #pragma unroll
                     for (int f = 0; f < 2; ++f)
 #pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            x[bk][nt][2 * f + e] += __shfl_xor_sync(FULL, x[bk][nt][2 * f + e], XOR);
+                        for (int e = 0; e < E; ++e) {
+                            float &v = x[bk][nt][2 * f + e];
+                            v *= part_scale;
+                            v += __shfl_xor_sync(FULL, v, XOR);
+                            if (RT == 1) v += __shfl_xor_sync(FULL, v, 2);
+                        }
                 }
             }
         }
-        if (a.scores != nullptr && !rest) {
+        if (a.scores != nullptr && head) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -412,12 +480,20 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
         // exponents against the reference m: y = x - m + DEC_PSHIFT, -inf where the row does not see the position.
         // m only has to keep 2^y inside fp16; it moves when some y passes DEC_YMAX, seldom after the first tile.
         const bool whole = pos0 + DEC_TILE <= L - n + 1;  // every row sees the whole tile
-        auto exponent = [&](int bk, int nt, int f, int e) {
-            const float v = fmaf(x[bk][nt][2 * f + e], cx[nt][e], off[nt][e]);
-            return whole || pos0 + 16 * bk + prow + 8 * f < vis[nt][e] ? v : -INFINITY;
-        };
         float y[2][NT][2][E];
-        bool over = false;
+        auto hide = [&]() {
+            if (whole) return;
+#pragma unroll
+            for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (pos0 + 16 * bk + prow + 8 * f >= vis[nt][e]) y[bk][nt][f][e] = -INFINITY;
+        };
+        float top = -INFINITY;
 #pragma unroll
         for (int bk = 0; bk < 2; ++bk)
 #pragma unroll
@@ -425,11 +501,15 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        y[bk][nt][f][e] = exponent(bk, nt, f, e);
-                        over |= y[bk][nt][f][e] > DEC_YMAX;
-                    }
-        if (__any_sync(FULL, over)) {
+                    for (int e = 0; e < E; ++e) y[bk][nt][f][e] = fmaf(x[bk][nt][2 * f + e], cx[nt][e], off[nt][e]);
+        hide();
+#pragma unroll
+        for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < E; ++e) top = max3f(top, y[bk][nt][0][e], y[bk][nt][1][e]);
+        if (__any_sync(FULL, top > DEC_YMAX)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -456,8 +536,9 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
 #pragma unroll
                     for (int bk = 0; bk < 2; ++bk)
 #pragma unroll
-                        for (int f = 0; f < 2; ++f) y[bk][nt][f][e] = exponent(bk, nt, f, e);
+                        for (int f = 0; f < 2; ++f) y[bk][nt][f][e] = fmaf(x[bk][nt][2 * f + e], cx[nt][e], off[nt][e]);
                 }
+            hide();
         }
         // weights, then O += V^T w^T block by block
 #pragma unroll
@@ -472,11 +553,11 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
                     for (int e = 0; e < E; ++e) pv[e] = ex2(y[bk][nt][f][e]);
                     uint32_t hw = half2_bits(pv[0], pv[1]);
                     const float2 r2 = __half22float2(*reinterpret_cast<const __half2 *>(&hw));
-                    if (PREC) {
+                    if (PREC == 2) {
 #pragma unroll
                         for (int e = 0; e < E; ++e) l[nt][e] += pv[e];
                         const uint32_t lw = half2_bits(pv[0] - r2.x, pv[1] - r2.y);
-                        hw = rest ? lw : hw;
+                        hw = part == 0 ? hw : part == 1 ? lw : 0u;
                     } else {  // the rounded weights are summed: numerator and denominator hold the same ones
                         l[nt][0] += r2.x;
                         if (E == 2) l[nt][E - 1] += r2.y;
@@ -490,9 +571,9 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
             VC::load(vst + (16 * bk + v0 + 8) * S::RB, gq, ra);
             VC::load(vst + (16 * bk + v1 + 8) * S::RB, gq, rc);
             VC::join(ra, rc, xb);
-            if (PREC) {
-#pragma unroll
-                for (int j = 0; j < VC::N; ++j) xa[j] = code_up(xa[j]), xb[j] = code_up(xb[j]);
+            if constexpr (PREC == 2) {
+                VC::about_mid(xa);
+                VC::about_mid(xb);
             }
 #pragma unroll
             for (int c = 0; c < D / 16; ++c)
@@ -522,18 +603,17 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int r = nt * RT + S::row(2 * tq + e);
-            const bool mine = S::used(2 * tq + e) && !rest;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c)
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
                     float v = o[c][nt][2 * f + e];
-                    if (PREC) v += __shfl_xor_sync(FULL, v, XOR);
+                    if (PREC == 2) v += __shfl_xor_sync(FULL, v, XOR);
                     // the codes' power of two and the weights' 2^DEC_PSHIFT
-                    v *= (float)(1 << ((PREC ? 10 : 24) - VC::pos(2 * c + f))) * (1.f / (float)(1 << DEC_PSHIFT));
-                    if (mine) js[(warp * S::ROWS + r) * D + gq * (D / 8) + 2 * c + f] = v;
+                    v *= (float)(1 << ((PREC == 2 ? 10 : 24) - VC::pos(2 * c + f))) * (1.f / (float)(1 << DEC_PSHIFT));
+                    if (head) js[(warp * S::ROWS + r) * D + gq * (D / 8) + 2 * c + f] = v;
                 }
-            if (gq == 0 && mine) {
+            if (gq == 0 && head) {
                 jm[warp * S::ROWS + r] = l[nt][e] == 0.f ? -INFINITY : m[nt][e];
                 jl[warp * S::ROWS + r] = l[nt][e] * (1.f / (float)(1 << DEC_PSHIFT));
             }
@@ -588,7 +668,7 @@ template <int D>
 __global__ void __launch_bounds__(CMB_THREADS)
     paged_combine_kernel(const PagedAttnDev a, int blocks)
 {
-    extern __shared__ float s_f[];  // a factor per part, or per row the base-2 log of the sum
+    extern __shared__ float s_f[];  // a factor per part, or per row the maximum and the sum's reciprocal
     const Paged &p = a.p;
     const int tid = threadIdx.x;
     const int64_t R = p.T * a.Hq;
@@ -610,7 +690,7 @@ __global__ void __launch_bounds__(CMB_THREADS)
 #pragma unroll 8
             for (int s = 0; s < a.splits; ++s) v = fmaf(a.part[(s * R + row) * D + d], s_f[s], v);
             const int k = cluster_of(a.kt.cv, h * D + d, a.kt.g, p.err);
-            store_elem(a.out, a.dtype, row * D + d, mt == -INFINITY ? 0.f : a.kt.sv[k] * (v - (float)a.kt.zv[k]));
+            store_elem(a.out, a.dtype, row * D + d, mt == -INFINITY ? 0.f : a.kt.sv[k] * (v - ((float)a.kt.zv[k] - a.mid)));
         }
         return;
     }
@@ -624,13 +704,14 @@ __global__ void __launch_bounds__(CMB_THREADS)
     for (int r = tid >> 5; r < rows; r += CMB_THREADS / 32) {
         float mt, lt;
         join_parts(a.ml, R, row_of(r), a.splits, mt, lt);
-        if ((tid & 31) == 0) s_f[r] = mt == -INFINITY ? INFINITY : mt + log2f(lt);
+        // (the log of the sum, added to a maximum of some thousands, would lose the sum's low bits)
+        if ((tid & 31) == 0) s_f[2 * r] = mt, s_f[2 * r + 1] = mt == -INFINITY ? 0.f : 1.f / lt;
     }
     __syncthreads();
     for (int pos = blk * CMB_KEYS + tid; pos < min(L, (blk + 1) * CMB_KEYS); pos += CMB_THREADS) {
         float w = 0.f;
         for (int r = 0; r < rows; ++r)
-            if (pos <= L - n + r / a.G) w += ex2(a.scores[row_of(r) * p.max_len + pos] - s_f[r]);
+            if (pos <= L - n + r / a.G) w = fmaf(ex2(a.scores[row_of(r) * p.max_len + pos] - s_f[2 * r]), s_f[2 * r + 1], w);
         const int page = paged_page(p, b, pos >> p.shift);
         if (page >= 0) a.weights[paged_row(page, a.H, h, p.shift) + (pos & ((1 << p.shift) - 1))] += w;
     }
@@ -639,15 +720,14 @@ __global__ void __launch_bounds__(CMB_THREADS)
 // ---- launch ----------------------------------------------------------------------------------------------
 namespace {
 struct DecPlan {
-    bool prec;
-    int rt, nt, splits;
+    int prec, rt, nt, splits;
 };
 constexpr int DEC_MAX_SPLITS = 64;
 DecPlan dec_plan(int Hq, int H, int dtype, int B, int max_q, int max_len, int weights, int num_sms)
 {
     DecPlan pl;
     const int64_t rows = (int64_t)max_q * (Hq / H);
-    pl.prec = weights || dtype != RPTQ_BF16;  // fp16's and fp32's results, and the sums, are finer than one part
+    pl.prec = dtype == RPTQ_F32 ? 2 : weights || dtype == RPTQ_F16 ? 1 : 0;
     pl.rt = rows == 1 ? 1 : pl.prec ? 4 : 8;
     pl.nt = rows <= pl.rt ? 1 : rows <= 2 * pl.rt ? 2 : 4;
     // parts: enough for three CTAs to an SM, each warp at least two tiles
@@ -676,7 +756,7 @@ size_t paged_decode_workspace(int64_t T, int Hq, int H, int D, int dtype, int B,
     return bytes;
 }
 
-template <int BITS, int D, int RT, int NT, bool PREC>
+template <int BITS, int D, int RT, int NT, int PREC>
 static cudaError_t launch_dec(const PagedAttnDev &d, const DecPlan &pl, int B, cudaStream_t stream)
 {
     using S = DecShape<BITS, D, RT, NT, PREC>;
@@ -686,18 +766,22 @@ static cudaError_t launch_dec(const PagedAttnDev &d, const DecPlan &pl, int B, c
     kern<<<(unsigned)((int64_t)B * d.H * pl.splits), DEC_THREADS, S::SMEM, stream>>>(d);
     return cudaGetLastError();
 }
+template <int BITS, int D, int RT, int PREC>
+static cudaError_t launch_dec_prec(const PagedAttnDev &d, const DecPlan &pl, int B, cudaStream_t stream)
+{
+    if (pl.rt == 1) return launch_dec<BITS, D, 1, 1, PREC>(d, pl, B, stream);
+    return pl.nt == 1   ? launch_dec<BITS, D, RT, 1, PREC>(d, pl, B, stream)
+           : pl.nt == 2 ? launch_dec<BITS, D, RT, 2, PREC>(d, pl, B, stream)
+                        : launch_dec<BITS, D, RT, 4, PREC>(d, pl, B, stream);
+}
 template <int BITS, int D>
 static cudaError_t launch_dec_rows(const PagedAttnDev &d, const DecPlan &pl, int B, cudaStream_t stream)
 {
-    if (pl.rt == 1)
-        return pl.prec ? launch_dec<BITS, D, 1, 1, true>(d, pl, B, stream) : launch_dec<BITS, D, 1, 1, false>(d, pl, B, stream);
-    if (pl.prec)
-        return pl.nt == 1   ? launch_dec<BITS, D, 4, 1, true>(d, pl, B, stream)
-               : pl.nt == 2 ? launch_dec<BITS, D, 4, 2, true>(d, pl, B, stream)
-                            : launch_dec<BITS, D, 4, 4, true>(d, pl, B, stream);
-    return pl.nt == 1   ? launch_dec<BITS, D, 8, 1, false>(d, pl, B, stream)
-           : pl.nt == 2 ? launch_dec<BITS, D, 8, 2, false>(d, pl, B, stream)
-                        : launch_dec<BITS, D, 8, 4, false>(d, pl, B, stream);
+    switch (pl.prec) {
+    case 2: return launch_dec_prec<BITS, D, 4, 2>(d, pl, B, stream);
+    case 1: return launch_dec_prec<BITS, D, 4, 1>(d, pl, B, stream);
+    default: return launch_dec_prec<BITS, D, 8, 0>(d, pl, B, stream);
+    }
 }
 
 cudaError_t launch_paged_decode(const PagedAttnArgs &a)
@@ -707,6 +791,7 @@ cudaError_t launch_paged_decode(const PagedAttnArgs &a)
     d.p = Paged{a.start, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, a.max_q, a.max_len, a.err};
     d.q = a.q, d.out = a.out, d.dtype = a.dtype, d.Hq = a.Hq, d.H = a.H, d.G = a.Hq / a.H, d.q_stride = a.q_stride;
     d.kq = a.kq, d.vq = a.vq, d.kt = a.kt, d.scale = a.scale, d.weights = a.weights, d.splits = pl.splits;
+    d.mid = pl.prec == 2 ? (float)(1 << (a.bits - 1)) : 0.f;
     const bool join = pl.splits > 1 || a.weights;
     if (join) {
         d.part = static_cast<float *>(a.ws);
@@ -718,7 +803,7 @@ cudaError_t launch_paged_decode(const PagedAttnArgs &a)
     if (e != cudaSuccess || !join) return e;
     const int blocks = a.weights ? std::max(1, (a.max_len + CMB_KEYS - 1) / CMB_KEYS) : 0;
     const unsigned grid = (unsigned)(a.T * a.Hq + (int64_t)a.B * a.H * blocks);
-    const size_t smem = std::max<size_t>(pl.splits, (size_t)a.max_q * d.G) * 4;
+    const size_t smem = std::max<size_t>(pl.splits, (size_t)a.max_q * d.G * 2) * 4;
     if (a.D == 128)
         paged_combine_kernel<128><<<grid, CMB_THREADS, smem, a.stream>>>(d, blocks);
     else
