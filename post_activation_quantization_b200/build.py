@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "librptq.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "calib.cu", "kmeans.cu", "ln_quant.cu", "kv_quant.cu", "dequant.cu", "kv_attention.cu", "explicit_reorder.cu", "linear.cu",
-           "kv_paged.cu", "kv_paged_attention.cu", "kv_paged_decode.cu"]
+           "kv_paged.cu", "kv_paged_attention.cu", "kv_paged_decode.cu", "kv_paged_chunk.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

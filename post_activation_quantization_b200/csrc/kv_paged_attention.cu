@@ -161,6 +161,7 @@ size_t paged_attention_workspace(int64_t T, int Hq, int H, int D, int dtype, int
 {
     if (paged_decode_takes(Hq, H, D, dtype, max_q, weights))
         return paged_decode_workspace(T, Hq, H, D, dtype, B, max_q, max_len, weights, num_sms);
+    if (D == 64 || D == 128) return paged_chunk_workspace(T, Hq, H, D, dtype, B, max_len, weights, num_sms);
     return weights ? (size_t)T * Hq * sizeof(float) : 0;
 }
 
@@ -182,6 +183,7 @@ static cudaError_t launch_paged_attention_t(const PagedAttnArgs &a)
 cudaError_t launch_paged_attention(const PagedAttnArgs &a)
 {
     if (paged_decode_takes(a.Hq, a.H, a.D, a.dtype, a.max_q, a.weights != nullptr)) return launch_paged_decode(a);
+    if (a.D == 64 || a.D == 128) return launch_paged_chunk(a);
     switch (a.dtype) {
     case RPTQ_F32: return a.bits == 4 ? launch_paged_attention_t<float, 4>(a) : launch_paged_attention_t<float, 3>(a);
     case RPTQ_F16: return a.bits == 4 ? launch_paged_attention_t<__half, 4>(a) : launch_paged_attention_t<__half, 3>(a);

@@ -71,6 +71,123 @@ __device__ __forceinline__ int cluster_of(const int32_t *cl, int c, int g, int *
     return 0;
 }
 
+// two codes (fp16 subnormals) times 2^14: exact, and normal numbers
+__device__ __forceinline__ uint32_t code_up(uint32_t v)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x74007400u));
+    return r;
+}
+// v 2^14 + c
+__device__ __forceinline__ uint32_t code_up_plus(uint32_t v, uint32_t c)
+{
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x74007400u), "r"(c));
+    return r;
+}
+// two codes at bit positions P0 and P1, times 2^14, about their middle
+template <int P0, int P1, int MID>
+__device__ __forceinline__ uint32_t code_about_mid(uint32_t v)
+{
+    constexpr uint32_t E = (MID == 8 ? 3 : 2) - 10 + 15;  // MID 2^(pos - 10) is a power of two: its exponent field less pos
+    return code_up_plus(v, (0x8000u | (E + P0) << 10) | (0x8000u | (E + P1) << 10) << 16);
+}
+__device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
+
+// ---- K: one thread's D / 4 consecutive codes of a row as D / 8 pairs --------------------------------------
+// Pair i holds code code(i, 0) at bit pos(i, 0) of the low half and code code(i, 1) at pos(i, 1) of the high
+// one.  4-bit: word j gives (8j, 8j+4), (8j+1, 8j+5), ... at positions 0, 4, 0, 4.  3-bit: a 32-bit window whose
+// first code is c holds codes c, c+1, c+2 at bits 0, 3, 6 and c+6, c+7, c+8 at 18, 21, 24; two windows three codes
+// apart cover 12 codes; the last 8 (D = 128) or 4 (D = 64) are laid into the halves first.
+template <int BITS, int D>
+struct KPairs {
+    static constexpr int N = D / 8;
+    __host__ __device__ static constexpr int code(int i, int half)
+    {
+        if (BITS == 4) return 8 * (i / 4) + i % 4 + 4 * half;
+        if (i < (D == 128 ? 12 : 6)) return 12 * (i / 6) + 3 * (i % 6 / 3) + i % 3 + 6 * half;
+        return D == 128 ? 24 + (i - 12) + 4 * half : 12 + (i - 6) + 2 * half;
+    }
+    __host__ __device__ static constexpr int pos(int i, int half)
+    {
+        if (BITS == 4) return 4 * (i & 1);
+        if (i < (D == 128 ? 12 : 6)) return 3 * (i % 3) + 2 * half;
+        return D == 128 ? (i == 15 ? 0 : 3 * (i - 12)) : 3 * (i - 6);
+    }
+    static constexpr int NW = (D / 4 * BITS + 31) / 32;  // words of a quarter
+    // the packed words of quarter t of the row at `a` (shared or global memory)
+    __device__ __forceinline__ static void read(const uint8_t *a, int t, uint32_t (&w)[NW])
+    {
+        if constexpr (BITS == 4 && D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(a + 16 * t);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else if constexpr (BITS == 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(a + 8 * t);
+            w[0] = v.x, w[1] = v.y;
+        } else if constexpr (D == 128) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(a + 12 * t);
+            w[0] = p[0], w[1] = p[1], w[2] = p[2];
+        } else {  // 48 bits at byte 6t
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(a + ((6 * t) & ~3));
+            const uint32_t wa = p[0], wb = p[1], s = 16 * (t & 1);
+            w[0] = __funnelshift_r(wa, wb, s);
+            w[1] = wb >> s;
+        }
+    }
+    __device__ __forceinline__ static void expand(const uint32_t (&w)[NW], uint32_t (&x)[N])
+    {
+        if constexpr (BITS == 4) {
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                const uint32_t u = w[j] >> 8;
+                x[4 * j] = w[j] & 0x000F000Fu;
+                x[4 * j + 1] = w[j] & 0x00F000F0u;
+                x[4 * j + 2] = u & 0x000F000Fu;
+                x[4 * j + 3] = u & 0x00F000F0u;
+            }
+        } else if constexpr (D == 128) {
+            window(w[0], &x[0]);
+            window(__funnelshift_r(w[0], w[1], 9), &x[3]);
+            window(__funnelshift_r(w[1], w[2], 4), &x[6]);
+            window(__funnelshift_r(w[1], w[2], 13), &x[9]);
+            const uint32_t v = w[2] >> 8;  // codes 24..31
+            const uint32_t u = (v & 0xFFFu) | ((v << 4) & 0xFFFFF000u);
+            x[12] = u & 0x00070007u;
+            x[13] = u & 0x00380038u;
+            x[14] = u & 0x01C001C0u;
+            x[15] = (u >> 9) & 0x00070007u;
+        } else {
+            window(w[0], &x[0]);
+            window(__funnelshift_r(w[0], w[1], 9), &x[3]);
+            const uint32_t v = w[1] >> 4;  // codes 12..15
+            const uint32_t u = (v & 0x3Fu) | ((v << 10) & 0xFFFF0000u);
+            x[6] = u & 0x00070007u;
+            x[7] = u & 0x00380038u;
+        }
+    }
+    __device__ __forceinline__ static void load(const uint8_t *a, int t, uint32_t (&x)[N])
+    {
+        uint32_t w[NW];
+        read(a, t, w);
+        expand(w, x);
+    }
+    // expanded pairs to 2^(pos - 10) (code - mid): exact normal numbers
+    template <int I = 0>
+    __device__ __forceinline__ static void about_mid(uint32_t (&x)[N])
+    {
+        if constexpr (I < N) {
+            x[I] = code_about_mid<pos(I, 0), pos(I, 1), 1 << (BITS - 1)>(x[I]);
+            about_mid<I + 1>(x);
+        }
+    }
+    __device__ __forceinline__ static void window(uint32_t w, uint32_t *x)
+    {
+        x[0] = w & 0x001C0007u;
+        x[1] = w & 0x00E00038u;
+        x[2] = w & 0x070001C0u;
+    }
+};
+
 // Arguments of the kernels for D = 64 and 128.
 struct PagedAttnDev {
     Paged p;
@@ -86,7 +203,8 @@ struct PagedAttnDev {
     // sum) [splits, T Hq, 2], and (with weights) the scores [T Hq, max_len], all base 2
     int splits;
     float *part, *ml, *scores;
-    float mid;  // what the codes of V have had taken off in `part`
+    float *stat;  // [T Hq, 2] maximum and reciprocal of the sum of each row, for the running sums of a chunk
+    float mid;    // what the codes of V have had taken off in `part`
 };
 
 // few rows to a K/V head (kv_paged_decode.cu)
@@ -94,5 +212,11 @@ bool paged_decode_takes(int Hq, int H, int D, int dtype, int max_q, int weights)
 size_t paged_decode_workspace(int64_t T, int Hq, int H, int D, int dtype, int B, int max_q, int max_len, int weights,
                               int num_sms);
 cudaError_t launch_paged_decode(const PagedAttnArgs &a);
+// joins the partial results of d.splits parts of the positions
+cudaError_t launch_paged_combine(const PagedAttnDev &d, int D, int B, bool weights, int max_rows, cudaStream_t stream);
+
+// many rows to a K/V head (kv_paged_chunk.cu)
+size_t paged_chunk_workspace(int64_t T, int Hq, int H, int D, int dtype, int B, int max_len, int weights, int num_sms);
+cudaError_t launch_paged_chunk(const PagedAttnArgs &a);
 
 }  // namespace rptq

@@ -1,0 +1,762 @@
+// kv_paged_chunk.cu -- paged attention of many query rows to a K/V head: prompts, chunks of prompts.
+//
+// Two contractions on the fifth-generation tensor cores, S = q' K^T and O += W V, with the softmax between
+// them in registers (one pass over the positions, running maximum and sum).  A CTA holds two tiles of 128
+// query rows (a row is a token and a head of the K/V head's group) and walks the positions in tiles of
+// 128; all 512 tensor-memory columns: S of both tiles (W replaces it in place, as fp16) and O of both.
+//   warps 0-3, 4-7    softmax of tile 0 / 1: one thread to a row
+//   warps 8-11        expand the packed codes of K and V into shared memory, as fp16
+//   warps 12, 13      issue the MMAs of tile 0 / 1
+// The two tiles share K and V and take turns on the tensor core: one's softmax runs while the other's
+// products do.  The codes come from global memory a tile ahead, are masked in place (kv_paged_attn.cuh) and
+// brought to small exact fp16 numbers by one fused multiply-add per two: K's relative to position 0's codes (a shift of all
+// scores of a row, which the softmax does not see; S then has the size of the scores' spread), V's about their middle.
+// Queries come from a first kernel as finished operand tiles, already scaled (q' = q s) and in the 128-byte swizzle.
+// Where the scores must be good to fp32 (fp32 queries, or running sums of weights), q' has two fp16 parts on one
+// grid and S takes two products; fp32 outputs have W in two parts as well.
+//
+// Running sums: a third kernel goes over the positions again with the rows' maxima and sums known: a tile of 128
+// positions is the row operand, S^T = K q'^T, so that a thread owns a position and adds its weights in registers,
+// row tile by row tile, in a fixed order.
+#include <algorithm>
+
+#include "kv_paged_attn.cuh"
+#include "tc.cuh"
+
+namespace rptq {
+
+constexpr int CH_M = 128, CH_KEYS = 128;
+constexpr int CH_SOFT_WARPS = 8, CH_PROD_WARPS = 4;
+constexpr int CH_PROD0 = CH_SOFT_WARPS, CH_MMA0 = CH_PROD0 + CH_PROD_WARPS;
+constexpr int CH_THREADS = 32 * (CH_MMA0 + 2);
+constexpr uint32_t CH_SLAB = CH_M * 128;  // 128 rows of 64 fp16
+// Weights are held as 2^y, y = x - m + CH_PSHIFT for a reference m that follows the running maximum (it moves when
+// some y passes CH_YMAX); fp16's smallest step is then 2^-(24 + CH_PSHIFT) of a weight at the reference.
+constexpr float CH_PSHIFT = 5.f, CH_YMAX = 15.f;
+
+// What the chunk kernels read besides PagedAttnDev.
+struct ChunkDev {
+    PagedAttnDev a;
+    const uint8_t *tiles;  // operand tiles of q': [H, slots, parts, D / 64, 128 rows, 128 bytes]
+    float *cx;             // [H, slots, 128]: base-2 score of a row = cx * S
+    int64_t slots;         // tile slots of a head
+};
+
+// Tile slots of a head: sequence b's tiles of `rows` rows start at slot start[b] * G / rows + b (each sequence ends
+// in at most one partial tile).  The sequence of a slot; the caller checks what it gets.
+__device__ __forceinline__ int64_t chunk_base(const Paged &p, int b, int G, int rows)
+{
+    return (int64_t)p.start[b] * G / rows + b;
+}
+__device__ __forceinline__ int chunk_sequence(const Paged &p, int64_t slot, int G, int rows)
+{
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (chunk_base(p, m, G, rows) <= slot)
+            lo = m;
+        else
+            hi = m;
+    }
+    return lo;
+}
+
+template <int BITS, int D>
+struct ChunkQ {
+    using KP = KPairs<BITS, D>;
+    // column of channel d in the order of the expanded codes, and the bit position of its code
+    __device__ static void column(int d, int &col, int &pos)
+    {
+        const int t = d / (D / 4), c = d % (D / 4);
+        col = pos = 0;
+#pragma unroll
+        for (int i = 0; i < KP::N; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (KP::code(i, e) == c) col = t * (D / 4) + 2 * i + e, pos = KP::pos(i, e);
+    }
+};
+
+// ---- the queries as operand tiles -----------------------------------------------------------------------
+// One CTA per (tile slot, head), a warp to a row.  PARTS = 1: fp16 of q' scaled so that the row's largest is in
+// [2^14, 2^15); 2: integers of 11 bits, the second 2^-11 of the first's unit and stored so.
+constexpr int CQ_THREADS = 256;
+template <int BITS, int D, int PARTS>
+__global__ void __launch_bounds__(CQ_THREADS)
+    paged_chunk_queries(const ChunkDev c, uint8_t *__restrict__ tiles)
+{
+    constexpr int CPL = D / 32;
+    constexpr uint32_t BYTES = PARTS * (D / 64) * CH_SLAB;
+    extern __shared__ __align__(16) uint8_t tile[];
+    __shared__ float s_s[D];
+    __shared__ int s_at[D];  // byte of channel d in a row of the tile (before the swizzle), pos << 16
+    const PagedAttnDev &a = c.a;
+    const Paged &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t slot = blockIdx.x % c.slots;
+    const int h = (int)(blockIdx.x / c.slots);
+    const int b = chunk_sequence(p, slot, a.G, CH_M);
+    int s0, n, L;
+    if (!paged_sequence(p, b, s0, n, L)) return;
+    const int64_t i = slot - chunk_base(p, b, a.G, CH_M);
+    const int64_t rows = (int64_t)n * a.G - i * CH_M;
+    if (i < 0 || rows <= 0) return;
+    for (int d = tid; d < D; d += CQ_THREADS) {
+        int col, pos;
+        ChunkQ<BITS, D>::column(d, col, pos);
+        s_s[d] = a.kt.sk[cluster_of(a.kt.ck, h * D + d, a.kt.g, p.err)];
+        s_at[d] = (col >> 6) * CH_SLAB + (col & 63) * 2 | pos << 24;
+    }
+    __syncthreads();
+    for (int r = warp; r < CH_M; r += CQ_THREADS / 32) {
+        const int64_t row = i * CH_M + r;
+        const int tok = (int)(row / a.G), j = (int)(row - (int64_t)tok * a.G);
+        float v[CPL], m = 0.f;
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            const int d = lane * CPL + k;
+            v[k] = r < rows ? load_elem(a.q, a.dtype, (int64_t)(s0 + tok) * a.q_stride + (int64_t)(h * a.G + j) * D + d) * s_s[d] : 0.f;
+            m = fmaxf(m, fabsf(v[k]));
+        }
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+        int ex = 0;
+        if (m > 0.f && m < INFINITY) frexpf(m, &ex);
+        ex = max(ex, -100);
+        const int grid = PARTS == 1 ? 15 : 11;
+        const float up = ldexpf(1.f, grid - ex);
+        if (lane == 0) c.cx[((int64_t)h * c.slots + slot) * CH_M + r] = ldexpf(a.scale * LOG2E, ex - grid + 10);
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            const int at = s_at[lane * CPL + k], pos = at >> 24;
+            const uint32_t o = (uint32_t)(at & 0xFFFFFF) + r * 128;
+            const uint32_t sw = o ^ ((r & 7) << 4);  // 16-byte piece c of a row sits at c ^ (row mod 8)
+            const float down = __uint_as_float((uint32_t)(127 - pos) << 23);  // 2^-pos
+            float f = v[k] * up;
+            const float g = PARTS == 1 ? f : rintf(f);
+            *reinterpret_cast<__half *>(tile + sw) = __float2half_rn(g * down);
+            if (PARTS == 2) {  // on the grid of 2^-11: exact in fp16
+                f = rintf((f - g) * 2048.f) * 0x1p-11f;
+                *reinterpret_cast<__half *>(tile + (D / 64) * CH_SLAB + sw) = __float2half_rn(f * down);
+            }
+        }
+    }
+    __syncthreads();
+    uint4 *dst = reinterpret_cast<uint4 *>(tiles + ((int64_t)h * c.slots + slot) * BYTES);
+    for (uint32_t k = tid; k < BYTES / 16; k += CQ_THREADS) dst[k] = reinterpret_cast<const uint4 *>(tile)[k];
+}
+
+// ---- expansion of the codes -----------------------------------------------------------------------------
+// A producer thread (0-127) has one quarter of every 32nd row of a tile.  The eight lanes of one 16-byte store phase
+// write eight different 16-byte columns of the swizzled tile: D = 128: two quarters (of one slab) of four rows;
+// D = 64: four quarters of two rows.
+template <int D>
+__device__ __forceinline__ void chunk_share(int pt, int &r0, int &t)
+{
+    if (D == 128)
+        t = (pt & 1) | ((pt >> 6) << 1), r0 = (pt >> 1) & 31;
+    else
+        t = pt & 3, r0 = pt >> 2;
+}
+// its four rows' packed words ...
+template <int BITS, int D>
+struct ChunkCodes {
+    using KP = KPairs<BITS, D>;
+    uint32_t w[4][KP::NW];
+    // rows r0, r0 + 32, ... of the tile at pos0; zeros past the sequence
+    __device__ __forceinline__ void read(const uint8_t *pages, const Paged &p, int b, int H, int h, int pos0, int L, int r0, int t)
+    {
+        constexpr int RB = D * BITS / 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int pos = pos0 + r0 + 32 * i;
+#pragma unroll
+            for (int k = 0; k < KP::NW; ++k) w[i][k] = 0;
+            if (pos < L) {
+                const int page = max(paged_page(p, b, pos >> p.shift), 0);
+                KP::read(pages + (paged_row(page, H, h, p.shift) + (pos & ((1 << p.shift) - 1))) * RB, t, w[i]);
+            }
+        }
+    }
+    // ... to shared memory: fp16 of D / 64 slabs of [128 rows, 128 bytes] in the 128-byte swizzle
+    template <typename F>
+    __device__ __forceinline__ void write(uint32_t tile, int r0, int t, F shape) const
+    {
+        constexpr int PIECES = KP::N / 4;  // 16-byte pieces of a quarter
+        const int slab = t * PIECES / 8, c0 = t * PIECES % 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x[KP::N];
+            KP::expand(w[i], x);
+            shape(x);
+            const int r = r0 + 32 * i;
+            const uint32_t row = tile + slab * CH_SLAB + r * 128;
+#pragma unroll
+            for (int j = 0; j < PIECES; ++j) {
+                const uint32_t at = row + (((c0 + j) ^ (r & 7)) << 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[4 * j]), "r"(x[4 * j + 1]),
+                             "r"(x[4 * j + 2]), "r"(x[4 * j + 3])
+                             : "memory");
+            }
+        }
+    }
+};
+
+// Position 0's codes of quarter t, negated, as the K expansion subtracts them.
+template <int BITS, int D>
+__device__ __forceinline__ void chunk_reference(const PagedAttnDev &a, int b, int h, int t, uint32_t (&ref)[KPairs<BITS, D>::N])
+{
+    const Paged &p = a.p;
+    const int page = max(paged_page(p, b, 0), 0);
+    KPairs<BITS, D>::load(a.kq + paged_row(page, a.H, h, p.shift) * (D * BITS / 8), t, ref);
+#pragma unroll
+    for (int i = 0; i < KPairs<BITS, D>::N; ++i) ref[i] = code_up(ref[i]) ^ 0x80008000u;
+}
+
+// ---- attention --------------------------------------------------------------------------------------------
+template <int D, int QP>
+struct ChunkShape {
+    static constexpr int SLABS = D / 64;
+    static constexpr uint32_t KV = SLABS * CH_SLAB;           // a K or V tile
+    static constexpr uint32_t QT = QP * SLABS * CH_SLAB;      // a query tile
+    static constexpr int STAGES = QP == 2 && D == 128 ? 1 : 2;  // what 227 KB leave
+    static constexpr uint32_t SMEM = 1024 + 2 * QT + 2 * STAGES * KV;
+    static constexpr uint32_t O_COL = 256;  // O of tile g at O_COL + g * D
+};
+
+template <int BITS, int D, int QP, int PP>
+__global__ void __launch_bounds__(CH_THREADS, 1)
+    paged_chunk_kernel(const ChunkDev c)
+{
+    using S = ChunkShape<D, QP>;
+    using KP = KPairs<BITS, D>;
+    constexpr int ST = S::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[4 * 2 + 3 * 2 + 1 + 2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ float s_sv[D], s_zv[D];
+    const PagedAttnDev &a = c.a;
+    const Paged &p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // CTA: (block of 256 rows, head, part of the positions); the blocks of a sequence from its last one (the longest) on
+    const int split = blockIdx.x % a.splits;
+    const int64_t u = blockIdx.x / a.splits;
+    const int h = (int)(u % a.H);
+    const int64_t slot2 = u / a.H;
+    const int b = chunk_sequence(p, slot2, a.G, 2 * CH_M);
+    int s0, n, L;
+    if (!paged_sequence(p, b, s0, n, L)) return;
+    const int R = n * a.G, blocks = (R + 2 * CH_M - 1) / (2 * CH_M);
+    const int64_t bi = slot2 - chunk_base(p, b, a.G, 2 * CH_M);
+    if (bi < 0 || bi >= blocks) return;
+    const int block = blocks - 1 - (int)bi;
+    const int row0 = block * 2 * CH_M, rows = min(2 * CH_M, R - row0);
+    const int nact = rows > CH_M ? 2 : 1;
+    const int64_t qslot = (int64_t)h * c.slots + chunk_base(p, b, a.G, CH_M) + 2 * block;
+    // tiles of positions: those that the last row sees, this part's share
+    const int vis = max(0, L - n + (row0 + rows - 1) / a.G + 1);
+    const int all = (vis + CH_KEYS - 1) / CH_KEYS;
+    const int j0 = (int)((int64_t)all * split / a.splits), j1 = (int)((int64_t)all * (split + 1) / a.splits);
+
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sQ = base, sK = base + 2 * S::QT, sV = sK + ST * S::KV;
+    const uint32_t bar = smem_u32(bars);
+    const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_empty = bar + 48;  // [2] each
+    const uint32_t s_full = bar + 64, p_full = bar + 80, o_done = bar + 96, q_full = bar + 112, drain = bar + 120;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(k_full + 8 * i, 32 * CH_PROD_WARPS);
+            mbar_init(v_full + 8 * i, 32 * CH_PROD_WARPS);
+            mbar_init(k_empty + 8 * i, nact);
+            mbar_init(v_empty + 8 * i, nact);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, CH_M);
+            mbar_init(o_done + 8 * i, 1);
+            mbar_init(drain + 8 * i, 1);
+        }
+        mbar_init(q_full, 1);
+        fence_mbar_init();
+    }
+    for (int d = tid; d < D; d += CH_THREADS) {
+        const int k = cluster_of(a.kt.cv, h * D + d, a.kt.g, p.err);
+        s_sv[d] = a.kt.sv[k];
+        s_zv[d] = (float)a.kt.zv[k] - (float)(1 << (BITS - 1));
+    }
+    if (warp == CH_MMA0) tc_alloc(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp < CH_SOFT_WARPS) {
+        const int g = warp >> 2, quad = warp & 3;
+        const int r = 32 * quad + lane, row = row0 + g * CH_M + r;  // the thread's row
+        const bool live = g < nact && row < R;
+        if (g < nact) {
+            const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+            const uint32_t tS = tmem + lanes + (uint32_t)g * CH_KEYS, tO = tmem + lanes + S::O_COL + (uint32_t)g * D;
+            const float cx = c.cx[(qslot + g) * CH_M + r];
+            const int vrow = live ? L - n + row / a.G + 1 : 0;                    // visible positions
+            const int vmin = L - n + (row0 + g * CH_M + 32 * quad) / a.G + 1;     // of the warp's first row
+            float m = -1e30f, off = live ? 1e30f : -INFINITY;
+            f32x2 l2 = mk2(0.f, 0.f);
+            bool ok = true;
+            for (int j = j0; j < j1 && ok; ++j) {
+                ok = __all_sync(FULL, mbar_wait_bounded(s_full + 8 * g, (j - j0) & 1, p.err));
+                if (!ok) break;
+                tc_fence_after();
+                const int pos0 = j * CH_KEYS;
+                const bool whole = pos0 + CH_KEYS <= vmin;
+                float top = -INFINITY;
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    uint32_t v[32];
+                    tc_ld32(tS + 32 * q4, v);
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) top = max3f(top, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (pos0 + 32 * q4 + k < vrow) top = fmaxf(top, __uint_as_float(v[k]));
+                    }
+                }
+                // cx > 0, so the largest score is cx * the largest S
+                const float ytop = fmaf(top, cx, off);
+                if (__any_sync(FULL, ytop > CH_YMAX)) {
+                    float f = 1.f;
+                    if (live && ytop > CH_PSHIFT) {
+                        const float mn = top * cx;
+                        f = ex2(m - mn);
+                        m = mn;
+                        off = CH_PSHIFT - mn;
+                        l2 = mul2(l2, mk2(f, f));
+                    }
+                    if (j > j0) {  // O of the tiles so far (its products are complete: the scores waited for them)
+#pragma unroll 1
+                        for (int q4 = 0; q4 < D / 32; ++q4) {
+                            uint32_t v[32];
+                            tc_ld32(tO + 32 * q4, v);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                            tc_st32(tO + 32 * q4, v);
+                        }
+                    }
+                }
+                const f32x2 cx2 = mk2(cx, cx), off2 = mk2(off, off);
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    uint32_t v[32], w[16], w2[16];
+                    tc_ld32(tS + 32 * q4, v);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        f32x2 y = fma2(mk2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), cx2, off2);
+                        if (!whole) {
+                            const int pos = pos0 + 32 * q4 + 2 * k;
+                            y = mk2(pos < vrow ? lo2(y) : -INFINITY, pos + 1 < vrow ? hi2(y) : -INFINITY);
+                        }
+                        const f32x2 e = mk2(ex2(lo2(y)), ex2(hi2(y)));
+                        l2 = add2(l2, e);
+                        w[k] = half2_bits(lo2(e), hi2(e));
+                        if (PP == 2) {
+                            const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                            w2[k] = half2_bits(lo2(e) - hf.x, hi2(e) - hf.y);
+                        }
+                    }
+                    // W over the 32 columns of S just read: 16 columns, its second part in the next 16
+                    tc_st16(tS + 32 * q4, w);
+                    if (PP == 2) tc_st16(tS + 32 * q4 + 16, w2);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                lin_arrive(p_full + 8 * g);
+            }
+            // ---- the row's result ----
+            if (ok && j1 > j0) ok = mbar_wait_bounded(o_done + 8 * g, (j1 - j0 - 1) & 1, p.err);
+            ok = __all_sync(FULL, ok);
+            tc_fence_after();
+            if (ok) {
+                const float l = (lo2(l2) + hi2(l2)) * 0x1p-5f;  // 2^-CH_PSHIFT
+                const bool sees = l > 0.f || l != l;
+                const int tok = row / a.G, jh = row - tok * a.G;
+                const int64_t orow = (int64_t)(s0 + tok) * a.Hq + h * a.G + jh;
+                const float inv = sees ? 1.f / l : 0.f;
+#pragma unroll 1
+                for (int q4 = 0; q4 < D / 32; ++q4) {
+                    uint32_t v[32];
+                    if (j1 > j0) {
+                        tc_ld32(tO + 32 * q4, v);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = 0;
+                    }
+                    if (!live) continue;
+                    float o[32];  // channels 32 q4 .. in order
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        constexpr int Q = D / 4;  // columns of a quarter
+                        const int i = k % Q / 2, e = k & 1;
+                        o[k / Q * Q + KP::code(i, e)] = __uint_as_float(v[k]) * ((float)(1 << (10 - KP::pos(i, e))) * 0x1p-5f);
+                    }
+                    if (a.part != nullptr) {
+                        float4 *dst = reinterpret_cast<float4 *>(a.part + ((int64_t)split * p.T * a.Hq + orow) * D + 32 * q4);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        continue;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = sees ? s_sv[32 * q4 + k] * (o[k] * inv - s_zv[32 * q4 + k]) : 0.f;
+                    if (a.dtype == RPTQ_F32) {
+                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * D + 32 * q4);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    } else {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const __nv_bfloat162 bb = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
+                            w[k] = a.dtype == RPTQ_F16 ? half2_bits(o[2 * k], o[2 * k + 1]) : *reinterpret_cast<const uint32_t *>(&bb);
+                        }
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + orow * D + 32 * q4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    }
+                }
+                if (live && a.part != nullptr) {
+                    float *ml = a.ml + ((int64_t)split * p.T * a.Hq + orow) * 2;
+                    ml[0] = sees ? m : -INFINITY;
+                    ml[1] = l;
+                } else if (live && a.stat != nullptr) {
+                    a.stat[2 * orow] = sees ? m : 0.f;
+                    a.stat[2 * orow + 1] = inv;
+                }
+            }
+        }
+    } else if (warp < CH_MMA0) {
+        // ---- producers ----
+        const int pt = tid - 32 * CH_PROD0;
+        if (pt == 0) {
+            const uint8_t *src = c.tiles + qslot * S::QT;
+            mbar_expect_tx(q_full, nact * S::QT);
+            for (uint32_t o = 0; o < nact * S::QT; o += CH_SLAB) bulk_g2s(sQ + o, src + o, CH_SLAB, q_full);
+        }
+        int r0, t;
+        chunk_share<D>(pt, r0, t);
+        bool ok = true;
+        if (j1 > j0) {
+            uint32_t ref[KP::N];
+            chunk_reference<BITS, D>(a, b, h, t, ref);
+            ChunkCodes<BITS, D> kc, vc;
+            kc.read(a.kq, p, b, a.H, h, j0 * CH_KEYS, L, r0, t);
+            vc.read(a.vq, p, b, a.H, h, j0 * CH_KEYS, L, r0, t);
+            for (int j = j0; j < j1 && ok; ++j) {
+                const int i = j - j0, st = i % ST;
+                const uint32_t free_ph = ((uint32_t)(i / ST) & 1) ^ 1;
+                if (!(ok = mbar_wait_bounded(k_empty + 8 * st, free_ph, p.err))) break;
+                kc.write(sK + st * S::KV, r0, t, [&](uint32_t(&x)[KP::N]) {
+#pragma unroll
+                    for (int k = 0; k < KP::N; ++k) x[k] = code_up_plus(x[k], ref[k]);
+                });
+                fence_proxy_async_smem();
+                lin_arrive(k_full + 8 * st);
+                if (j + 1 < j1) kc.read(a.kq, p, b, a.H, h, (j + 1) * CH_KEYS, L, r0, t);
+                if (!(ok = mbar_wait_bounded(v_empty + 8 * st, free_ph, p.err))) break;
+                vc.write(sV + st * S::KV, r0, t, [&](uint32_t(&x)[KP::N]) { KP::about_mid(x); });
+                fence_proxy_async_smem();
+                lin_arrive(v_full + 8 * st);
+                if (j + 1 < j1) vc.read(a.vq, p, b, a.H, h, (j + 1) * CH_KEYS, L, r0, t);
+            }
+        }
+        if (pt == 0) mbar_wait_bounded(q_full, 0, p.err);  // no copy may be in flight when the CTA ends
+    } else {
+        const int g = warp - CH_MMA0;
+        if (lane == 0 && g < nact) {
+            constexpr uint32_t qk = f16_idesc(CH_M, CH_KEYS), pv = f16_idesc(CH_M, D) | IDESC_B_MN;
+            const uint32_t tS = tmem + (uint32_t)g * CH_KEYS, tO = tmem + S::O_COL + (uint32_t)g * D;
+            const uint32_t q0 = sQ + g * S::QT;
+            bool ok = mbar_wait_bounded(q_full, 0, p.err);
+            for (int j = j0; j < j1 && ok; ++j) {
+                const int i = j - j0, st = i % ST;
+                const uint32_t ph = (uint32_t)(i / ST) & 1;
+                // S (and W in its place) is free once the products that read it are complete
+                if (i > 0 && !(ok = mbar_wait_bounded(o_done + 8 * g, (i - 1) & 1, p.err))) break;
+                if (!(ok = mbar_wait_bounded(k_full + 8 * st, ph, p.err))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int part = 0; part < QP; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma_f16_ss(tS, sw128_desc(q0 + (part * S::SLABS + kk / 4) * CH_SLAB) + 2 * (kk % 4),
+                                      sw128_desc(sK + st * S::KV + kk / 4 * CH_SLAB) + 2 * (kk % 4), qk, (part | kk) != 0);
+                tc_commit(k_empty + 8 * st);
+                tc_commit(s_full + 8 * g);
+                if (!(ok = mbar_wait_bounded(p_full + 8 * g, i & 1, p.err))) break;
+                if (!(ok = mbar_wait_bounded(v_full + 8 * st, ph, p.err))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int part = 0; part < PP; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < CH_KEYS / 16; ++kk)
+                        tc_mma_f16_ts(tO, tS + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part,
+                                      sw128_mn_desc(sV + st * S::KV + kk * 2048, CH_SLAB), pv, i > 0 || (part | kk) != 0);
+                tc_commit(v_empty + 8 * st);
+                tc_commit(o_done + 8 * g);
+            }
+            tc_commit(drain + 8 * g);  // tensor memory is released below: every issued product first
+            mbar_wait_bounded(drain + 8 * g, 0, p.err);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == CH_MMA0) {
+        tc_fence_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+// ---- running sums -------------------------------------------------------------------------------------------
+// One CTA per (sequence, head, tile of 128 positions).  Warps 0-3 and 4-7 take the row tiles in turn, a thread to a position;
+// warp 8 issues the MMAs, warp 9 the copies of the query tiles (two in flight).
+constexpr int CW_THREADS = 320;
+template <int D>
+struct WeightShape {
+    static constexpr uint32_t QT = 2 * (D / 64) * CH_SLAB, KT = (D / 64) * CH_SLAB;
+    static constexpr uint32_t SMEM = 1024 + 2 * QT + KT;
+};
+template <int BITS, int D>
+__global__ void __launch_bounds__(CW_THREADS, 1)
+    paged_chunk_weights(const ChunkDev c, int blocks)
+{
+    using S = WeightShape<D>;
+    using KP = KPairs<BITS, D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[9];
+    __shared__ uint32_t tmem_slot;
+    __shared__ float4 s_row[2][2][CH_M];  // [group][turn][row]: cx, maximum, 1 / sum, visible positions
+    __shared__ float s_sum[CH_M];
+    const PagedAttnDev &a = c.a;
+    const Paged &p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int blk = blockIdx.x % blocks, bh = blockIdx.x / blocks, b = bh / a.H, h = bh % a.H;
+    int s0, n, L;
+    if (!paged_sequence(p, b, s0, n, L)) return;
+    const int R = n * a.G, pos0 = blk * CH_KEYS;
+    if (R == 0 || pos0 >= L) return;
+    const int64_t qslot = (int64_t)h * c.slots + chunk_base(p, b, a.G, CH_M);
+    const int i0 = (int)((int64_t)max(0, pos0 - (L - n)) * a.G / CH_M), i1 = (R + CH_M - 1) / CH_M;  // row tiles that see the block
+
+    const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u, sK = sQ + 2 * S::QT;
+    const uint32_t bar = smem_u32(bars);
+    const uint32_t q_full = bar, q_empty = bar + 16, s_full = bar + 32, s_free = bar + 48, drain = bar + 64;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + 8 * i, 1);
+            mbar_init(q_empty + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(s_free + 8 * i, CH_M);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 8) tc_alloc(smem_u32(&tmem_slot), 256);
+    if (warp < 4) {
+        int r0, t;
+        chunk_share<D>(tid, r0, t);
+        uint32_t ref[KP::N];
+        chunk_reference<BITS, D>(a, b, h, t, ref);
+        ChunkCodes<BITS, D> kc;
+        kc.read(a.kq, p, b, a.H, h, pos0, L, r0, t);
+        kc.write(sK, r0, t, [&](uint32_t(&x)[KP::N]) {
+#pragma unroll
+            for (int k = 0; k < KP::N; ++k) x[k] = code_up_plus(x[k], ref[k]);
+        });
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp < 8) {
+        const int g = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
+        const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)g * CH_M;
+        const int pos = pos0 + r;
+        float w0 = 0.f, w1 = 0.f;
+        bool ok = true;
+        for (int i = i0 + g, k = 0; i < i1; i += 2, ++k) {  // every warp takes every turn: the barrier counts them
+            const int row = i * CH_M + r;
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < R) {
+                const int tok = row / a.G, j = row - tok * a.G;
+                const int64_t orow = (int64_t)(s0 + tok) * a.Hq + h * a.G + j;
+                f = make_float4(c.cx[(qslot + i) * CH_M + r], a.stat[2 * orow], a.stat[2 * orow + 1],
+                                __int_as_float(L - n + tok + 1));
+            }
+            s_row[g][k & 1][r] = f;
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+            ok = ok && __all_sync(FULL, mbar_wait_bounded(s_full + 8 * g, k & 1, p.err));
+            if (!ok) continue;
+            tc_fence_after();
+            const bool whole = pos0 + CH_KEYS <= L - n + i * CH_M / a.G + 1;  // every row of the tile sees every position
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+                uint32_t v[32];
+                tc_ld32(tS + 32 * q4, v);
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                    const float4 s = s_row[g][k & 1][32 * q4 + q];
+                    float e = ex2(fmaf(__uint_as_float(v[q]), s.x, -s.y));
+                    if (!whole && pos >= __float_as_int(s.w)) e = 0.f;
+                    if (q & 1)
+                        w1 = fmaf(e, s.z, w1);
+                    else
+                        w0 = fmaf(e, s.z, w0);
+                }
+            }
+            tc_fence_before();
+            lin_arrive(s_free + 8 * g);
+        }
+        const float w = w0 + w1;
+        if (g == 1) s_sum[r] = w;
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+        if (g == 0 && pos < L) {
+            const int page = paged_page(p, b, pos >> p.shift);
+            if (page >= 0) a.weights[paged_row(page, a.H, h, p.shift) + (pos & ((1 << p.shift) - 1))] += w + s_sum[r];
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            constexpr uint32_t id = f16_idesc(CH_M, CH_M);
+            for (int i = i0, k = 0; i < i1; ++i, ++k) {
+                const int st = k & 1;
+                if (!mbar_wait_bounded(q_full + 8 * st, (k >> 1) & 1, p.err)) break;
+                if (!mbar_wait_bounded(s_free + 8 * st, ((k >> 1) & 1) ^ 1, p.err)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma_f16_ss(tmem + st * CH_M, sw128_desc(sK + kk / 4 * CH_SLAB) + 2 * (kk % 4),
+                                      sw128_desc(sQ + st * S::QT + (part * (D / 64) + kk / 4) * CH_SLAB) + 2 * (kk % 4), id,
+                                      (part | kk) != 0);
+                tc_commit(q_empty + 8 * st);
+                tc_commit(s_full + 8 * st);
+            }
+            tc_commit(drain);
+            mbar_wait_bounded(drain, 0, p.err);
+        }
+        __syncwarp();
+    } else {
+        if (lane == 0) {
+            int issued = 0;
+            for (int i = i0, k = 0; i < i1; ++i, ++k) {
+                const int st = k & 1;
+                if (!mbar_wait_bounded(q_empty + 8 * st, ((k >> 1) & 1) ^ 1, p.err)) break;
+                const uint8_t *src = c.tiles + (qslot + i) * S::QT;
+                mbar_expect_tx(q_full + 8 * st, S::QT);
+                for (uint32_t o = 0; o < S::QT; o += CH_SLAB) bulk_g2s(sQ + st * S::QT + o, src + o, CH_SLAB, q_full + 8 * st);
+                issued = k + 1;
+            }
+            for (int k = max(0, issued - 2); k < issued; ++k)  // no copy may be in flight when the CTA ends
+                mbar_wait_bounded(q_full + 8 * (k & 1), (k >> 1) & 1, p.err);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tc_dealloc(tmem, 256);
+    }
+}
+
+// ---- launch ---------------------------------------------------------------------------------------------------
+namespace {
+struct ChunkPlan {
+    int qp, splits;
+    int64_t slots, slots2;
+    size_t tiles, cx, stat, part, total;  // offsets into the workspace, its size
+};
+ChunkPlan chunk_plan(int64_t T, int Hq, int H, int D, int dtype, int B, int max_len, int weights, int num_sms)
+{
+    ChunkPlan pl;
+    const int64_t G = Hq / H, R = T * Hq;
+    pl.qp = weights || dtype == RPTQ_F32 ? 2 : 1;
+    pl.slots = T * G / CH_M + B;
+    pl.slots2 = T * G / (2 * CH_M) + B;
+    // the positions are split where the blocks of 256 rows leave SMs without one, each part at least four tiles
+    const int64_t units = std::max<int64_t>(1, T * G / (2 * CH_M)) * H;
+    pl.splits = (int)std::max<int64_t>(1, std::min<int64_t>({num_sms / units, max_len / (4 * CH_KEYS), 16}));
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    pl.tiles = 0;
+    pl.cx = up((size_t)H * pl.slots * pl.qp * (D / 64) * CH_SLAB);
+    pl.stat = pl.cx + up((size_t)H * pl.slots * CH_M * 4);
+    pl.part = pl.stat + (weights ? up((size_t)R * 8) : 0);
+    pl.total = pl.part + (pl.splits > 1 ? (size_t)pl.splits * R * (D + 2) * 4 : 0);
+    return pl;
+}
+
+template <int BITS, int D, int QP, int PP>
+cudaError_t launch_chunk(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles, int B, int max_rows, cudaStream_t stream)
+{
+    constexpr size_t qsmem = (size_t)QP * (D / 64) * CH_SLAB;
+    cudaError_t e = kernel_smem((const void *)paged_chunk_queries<BITS, D, QP>, qsmem);
+    if (e == cudaSuccess) e = kernel_smem((const void *)paged_chunk_kernel<BITS, D, QP, PP>, ChunkShape<D, QP>::SMEM);
+    if (e != cudaSuccess) return e;
+    paged_chunk_queries<BITS, D, QP><<<(unsigned)(pl.slots * c.a.H), CQ_THREADS, qsmem, stream>>>(c, tiles);
+    paged_chunk_kernel<BITS, D, QP, PP>
+        <<<(unsigned)(pl.slots2 * c.a.H * pl.splits), CH_THREADS, ChunkShape<D, QP>::SMEM, stream>>>(c);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (pl.splits > 1 && (e = launch_paged_combine(c.a, D, B, false, max_rows, stream)) != cudaSuccess) return e;
+    if (c.a.weights != nullptr) {
+        if constexpr (QP == 2) {
+            if ((e = kernel_smem((const void *)paged_chunk_weights<BITS, D>, WeightShape<D>::SMEM)) != cudaSuccess) return e;
+            const int blocks = (c.a.p.max_len + CH_KEYS - 1) / CH_KEYS;
+            paged_chunk_weights<BITS, D>
+                <<<(unsigned)((int64_t)B * c.a.H * blocks), CW_THREADS, WeightShape<D>::SMEM, stream>>>(c, blocks);
+        }
+    }
+    return cudaGetLastError();
+}
+template <int BITS, int D>
+cudaError_t launch_chunk_prec(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles, int B, int max_rows, cudaStream_t stream)
+{
+    if (c.a.dtype == RPTQ_F32) return launch_chunk<BITS, D, 2, 2>(c, pl, tiles, B, max_rows, stream);
+    if (pl.qp == 2) return launch_chunk<BITS, D, 2, 1>(c, pl, tiles, B, max_rows, stream);
+    return launch_chunk<BITS, D, 1, 1>(c, pl, tiles, B, max_rows, stream);
+}
+}  // namespace
+
+size_t paged_chunk_workspace(int64_t T, int Hq, int H, int D, int dtype, int B, int max_len, int weights, int num_sms)
+{
+    return chunk_plan(T, Hq, H, D, dtype, B, max_len, weights, num_sms).total;
+}
+
+cudaError_t launch_paged_chunk(const PagedAttnArgs &a)
+{
+    const ChunkPlan pl = chunk_plan(a.T, a.Hq, a.H, a.D, a.dtype, a.B, a.max_len, a.weights != nullptr, a.num_sms);
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    ChunkDev c{};
+    PagedAttnDev &d = c.a;
+    d.p = Paged{a.start, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, a.max_q, a.max_len, a.err};
+    d.q = a.q, d.out = a.out, d.dtype = a.dtype, d.Hq = a.Hq, d.H = a.H, d.G = a.Hq / a.H, d.q_stride = a.q_stride;
+    d.kq = a.kq, d.vq = a.vq, d.kt = a.kt, d.scale = a.scale, d.weights = a.weights, d.splits = pl.splits;
+    d.mid = (float)(1 << (a.bits - 1));
+    if (a.weights) d.stat = reinterpret_cast<float *>(ws + pl.stat);
+    if (pl.splits > 1) {
+        d.part = reinterpret_cast<float *>(ws + pl.part);
+        d.ml = d.part + (int64_t)pl.splits * a.T * a.Hq * a.D;
+    }
+    uint8_t *tiles = ws + pl.tiles;
+    c.tiles = tiles;
+    c.cx = reinterpret_cast<float *>(ws + pl.cx);
+    c.slots = pl.slots;
+    const int max_rows = a.max_q * d.G;
+    if (a.bits == 4)
+        return a.D == 128 ? launch_chunk_prec<4, 128>(c, pl, tiles, a.B, max_rows, a.stream)
+                          : launch_chunk_prec<4, 64>(c, pl, tiles, a.B, max_rows, a.stream);
+    return a.D == 128 ? launch_chunk_prec<3, 128>(c, pl, tiles, a.B, max_rows, a.stream)
+                      : launch_chunk_prec<3, 64>(c, pl, tiles, a.B, max_rows, a.stream);
+}
+
+}  // namespace rptq

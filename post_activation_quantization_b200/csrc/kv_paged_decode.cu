@@ -51,99 +51,6 @@ __device__ __forceinline__ uint32_t mat_trans(uint32_t v)
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// two codes (fp16 subnormals) times 2^14: exact, and normal numbers
-__device__ __forceinline__ uint32_t code_up(uint32_t v)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x74007400u));
-    return r;
-}
-// the same less 2^14 * mid * 2^(pos - 24): two codes about their middle
-template <int POS, int MID>
-__device__ __forceinline__ uint32_t code_about_mid(uint32_t v)
-{
-    constexpr int LOG = MID == 8 ? 3 : 2;  // MID * 2^(POS - 10) is a power of two
-    constexpr uint32_t H = 0x8000u | (uint32_t)(POS + LOG - 10 + 15) << 10;
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x74007400u), "r"(H | H << 16));
-    return r;
-}
-__device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
-
-// ---- K: one thread's D / 4 consecutive codes of a row as D / 8 pairs --------------------------------------
-// Pair i holds code code(i, 0) at bit pos(i, 0) of the low half and code code(i, 1) at pos(i, 1) of the high
-// one.  4-bit: word j gives (8j, 8j+4), (8j+1, 8j+5), ... at positions 0, 4, 0, 4.  3-bit: a 32-bit window whose
-// first code is c holds codes c, c+1, c+2 at bits 0, 3, 6 and c+6, c+7, c+8 at 18, 21, 24; two windows three codes
-// apart cover 12 codes; the last 8 (D = 128) or 4 (D = 64) are laid into the halves first.
-template <int BITS, int D>
-struct KPairs {
-    static constexpr int N = D / 8;
-    __host__ __device__ static constexpr int code(int i, int half)
-    {
-        if (BITS == 4) return 8 * (i / 4) + i % 4 + 4 * half;
-        if (i < (D == 128 ? 12 : 6)) return 12 * (i / 6) + 3 * (i % 6 / 3) + i % 3 + 6 * half;
-        return D == 128 ? 24 + (i - 12) + 4 * half : 12 + (i - 6) + 2 * half;
-    }
-    __host__ __device__ static constexpr int pos(int i, int half)
-    {
-        if (BITS == 4) return 4 * (i & 1);
-        if (i < (D == 128 ? 12 : 6)) return 3 * (i % 3) + 2 * half;
-        return D == 128 ? (i == 15 ? 0 : 3 * (i - 12)) : 3 * (i - 6);
-    }
-    // the packed codes of the lane's quarter of the row at `a`
-    __device__ __forceinline__ static void load(const uint8_t *a, int t, uint32_t (&x)[N])
-    {
-        if constexpr (BITS == 4) {
-            uint32_t w[D / 32];
-            if constexpr (D == 128) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(a + 16 * t);
-                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-            } else {
-                const uint2 v = *reinterpret_cast<const uint2 *>(a + 8 * t);
-                w[0] = v.x, w[1] = v.y;
-            }
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                const uint32_t u = w[j] >> 8;
-                x[4 * j] = w[j] & 0x000F000Fu;
-                x[4 * j + 1] = w[j] & 0x00F000F0u;
-                x[4 * j + 2] = u & 0x000F000Fu;
-                x[4 * j + 3] = u & 0x00F000F0u;
-            }
-        } else if constexpr (D == 128) {
-            const uint8_t *p = a + 12 * t;
-            const uint32_t x0 = lds32(p), x1 = lds32(p + 4), x2 = lds32(p + 8);
-            window(x0, &x[0]);
-            window(__funnelshift_r(x0, x1, 9), &x[3]);
-            window(__funnelshift_r(x1, x2, 4), &x[6]);
-            window(__funnelshift_r(x1, x2, 13), &x[9]);
-            const uint32_t w = x2 >> 8;  // codes 24..31
-            const uint32_t u = (w & 0xFFFu) | ((w << 4) & 0xFFFFF000u);
-            x[12] = u & 0x00070007u;
-            x[13] = u & 0x00380038u;
-            x[14] = u & 0x01C001C0u;
-            x[15] = (u >> 9) & 0x00070007u;
-        } else {
-            const uint8_t *p = a + ((6 * t) & ~3);  // 48 bits at byte 6t
-            const uint32_t s = 16 * (t & 1);
-            const uint32_t wa = lds32(p), wb = lds32(p + 4);
-            const uint32_t y0 = __funnelshift_r(wa, wb, s), y1 = wb >> s;
-            window(y0, &x[0]);
-            window(__funnelshift_r(y0, y1, 9), &x[3]);
-            const uint32_t w = y1 >> 4;  // codes 12..15
-            const uint32_t u = (w & 0x3Fu) | ((w << 10) & 0xFFFF0000u);
-            x[6] = u & 0x00070007u;
-            x[7] = u & 0x00380038u;
-        }
-    }
-    __device__ __forceinline__ static void window(uint32_t w, uint32_t *x)
-    {
-        x[0] = w & 0x001C0007u;
-        x[1] = w & 0x00E00038u;
-        x[2] = w & 0x070001C0u;
-    }
-};
-
 // ---- V: one thread's D / 8 consecutive codes of two rows, code by code -----------------------------------
 // x[i] holds code i of row a in the low half and of row b in the high half, both at bit pos(i).
 template <int BITS, int D>
@@ -154,7 +61,7 @@ struct VCodes {
     __device__ __forceinline__ static void about_mid(uint32_t (&x)[N])
     {
         if constexpr (I < N) {
-            x[I] = code_about_mid<pos(I), MID>(x[I]);
+            x[I] = code_about_mid<pos(I), pos(I), MID>(x[I]);
             about_mid<I + 1>(x);
         }
     }
@@ -684,6 +591,10 @@ __global__ void __launch_bounds__(CMB_THREADS)
             s_f[s] = ms == -INFINITY ? 0.f : ex2(ms - mt) / lt;
         }
         __syncthreads();
+        if (a.stat != nullptr && tid == 0) {
+            a.stat[2 * row] = mt == -INFINITY ? 0.f : mt;
+            a.stat[2 * row + 1] = mt == -INFINITY ? 0.f : 1.f / lt;
+        }
         const int h = (int)(row % a.Hq) / a.G;
         for (int d = tid; d < D; d += CMB_THREADS) {
             float v = 0.f;
@@ -801,13 +712,18 @@ cudaError_t launch_paged_decode(const PagedAttnArgs &a)
     cudaError_t e = a.bits == 4 ? (a.D == 128 ? launch_dec_rows<4, 128>(d, pl, a.B, a.stream) : launch_dec_rows<4, 64>(d, pl, a.B, a.stream))
                                 : (a.D == 128 ? launch_dec_rows<3, 128>(d, pl, a.B, a.stream) : launch_dec_rows<3, 64>(d, pl, a.B, a.stream));
     if (e != cudaSuccess || !join) return e;
-    const int blocks = a.weights ? std::max(1, (a.max_len + CMB_KEYS - 1) / CMB_KEYS) : 0;
-    const unsigned grid = (unsigned)(a.T * a.Hq + (int64_t)a.B * a.H * blocks);
-    const size_t smem = std::max<size_t>(pl.splits, (size_t)a.max_q * d.G * 2) * 4;
-    if (a.D == 128)
-        paged_combine_kernel<128><<<grid, CMB_THREADS, smem, a.stream>>>(d, blocks);
+    return launch_paged_combine(d, a.D, a.B, a.weights != nullptr, a.max_q * d.G, a.stream);
+}
+
+cudaError_t launch_paged_combine(const PagedAttnDev &d, int D, int B, bool weights, int max_rows, cudaStream_t stream)
+{
+    const int blocks = weights ? std::max(1, (d.p.max_len + CMB_KEYS - 1) / CMB_KEYS) : 0;
+    const unsigned grid = (unsigned)(d.p.T * d.Hq + (int64_t)B * d.H * blocks);
+    const size_t smem = std::max<size_t>(d.splits, weights ? (size_t)max_rows * 2 : 0) * 4;
+    if (D == 128)
+        paged_combine_kernel<128><<<grid, CMB_THREADS, smem, stream>>>(d, blocks);
     else
-        paged_combine_kernel<64><<<grid, CMB_THREADS, smem, a.stream>>>(d, blocks);
+        paged_combine_kernel<64><<<grid, CMB_THREADS, smem, stream>>>(d, blocks);
     return cudaGetLastError();
 }
 

@@ -14,7 +14,9 @@ Attention's bars follow from the arithmetic.  With q'_d = q_d s_d and the code k
     (2^-21, or 2^-10 for a numerator and a denominator of 11 bits) and, below the smallest part, by
     2^-24 of the row's largest weight;
   * sums over L positions take at most L/4 + 64 fp32 roundings, each counted 4 times;
-  * out_d = s_d (sum_p w_p k_pd - z_d): errors are relative to s_d (sum_p w_p k_pd + |z_d|) = `mag`;
+  * out_d = s_d (sum_p w_p k_pd - z_d), where a kernel may take the codes about their middle h = 2^(bits-1), as
+    s_d (sum_p w_p (k_pd - h) - (z_d - h)): the rounded sum is then up to sum_p w_p |k_pd - h| <= h whatever sum_p w_p k_pd
+    is (all codes 0: -h), so errors are relative to s_d (sum_p w_p k_pd + |z_d| + 2 h) = `mag`;
   * the output is rounded to its type: half a step, eps/2, relative."""
 import math
 
@@ -116,7 +118,7 @@ def check_attention(c, q, out, dtype, scale=0.0, weights=None, k=None, v=None):
         sums = 4 * (L / 4 + 64) * U
         rel = np.expm1(2 * e_x) + 2.0 ** -21 + rw + sums  # [Hq, n]
         qmax = 2 ** c.bits - 1
-        mag = sv * np.abs(np.einsum("anp,pad->nad", w, V / sv + zv)) + sv * np.abs(zv)
+        mag = sv * np.abs(np.einsum("anp,pad->nad", w, V / sv + zv)) + sv * (np.abs(zv) + 2 ** c.bits)
         tol = rel.T[..., None] * mag + sv * qmax * L * U * (w.max(axis=2).T[..., None] * 2) + 8 * U * mag
         tol = tol + np.abs(ref[rows]) * torch.finfo(TD[dtype]).eps / 2 * (1 + 1e-6) + 1e-30
         if dtype == "f16":
