@@ -17,6 +17,7 @@ LIB = os.path.join(PKG, "librptq.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "calib.cu", "kmeans.cu", "ln_quant.cu", "kv_quant.cu", "dequant.cu", "kv_attention.cu", "explicit_reorder.cu", "linear.cu",
            "kv_paged.cu", "kv_paged_attention.cu", "kv_paged_decode.cu", "kv_paged_chunk.cu"]
+MARSHAL = os.path.join(PKG, "_marshal.so")  # argument marshalling of the paged-cache calls (host code only)
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -40,6 +41,25 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_marshal(force: bool = False) -> str:
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not force and not _stale(MARSHAL, [src, os.path.join(ROOT, "include", "rptq.h")]):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    home, cuda = os.path.dirname(torch.__file__), os.path.dirname(os.path.dirname(nvcc()))
+    inc = [f for d in (os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                       os.path.join(cuda, "include"), sysconfig.get_paths()["include"]) for f in ("-isystem", d)]
+    lib = os.path.join(home, "lib")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+                           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, src, "-o", tmp,
+                           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"])
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, jobs: int = 8) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -60,11 +80,13 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int = 8) -> st
         return cmd, r
 
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        marshal = ex.submit(build_marshal, force)
         for cmd, r in ex.map(run, cmds):
             if ptxas_verbose or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
                 raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
+        marshal.result()
     if force or cmds or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.check_call([cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])

@@ -381,57 +381,33 @@ def rptq_reordered_linear(codes, C: int, bits: int, w_prep, w_bias, w_lambda, w_
 
 
 # ---------------------------------------------------------------------------------------------
-# The paged packed K/V cache
-def _need(ok, where: str):
-    if not ok:
-        raise RptqError(RPTQ_ERR_INVALID_ARG, where)
+# The paged packed K/V cache.  The tensors of these calls are checked and handed over by compiled code
+# (csrc/marshal.cpp): type, shape, layout (contiguous; q's, k_new's and v_new's rows may be slices of a wider
+# tensor) and device (the current one).  A tensor that does not fit raises RptqError (RPTQ_ERR_INVALID_ARG).
+_marshal = None
 
 
-def _arg(t: torch.Tensor | None, dtype, shape, dev: int, where: str):
-    """Address of a contiguous tensor that must have this type, shape and device index."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise RptqError(RPTQ_ERR_INVALID_ARG, where)
-    return t.data_ptr()
+def _paged():
+    """The marshalling module, bound to the loaded library (raises if it is absent)."""
+    global _marshal
+    if _marshal is None:
+        import importlib.util
+        path = os.path.join(_PKG, "_marshal.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m post_activation_quantization_b200.build`")
+        spec = importlib.util.spec_from_file_location("_marshal", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.bind(*(ctypes.cast(f, _P).value for f in (L.rptq_kv_paged_append, L.rptq_kv_paged_dequant,
+                                                    L.rptq_kv_paged_attention_workspace_size, L.rptq_kv_paged_attention,
+                                                    L.rptq_kv_paged_evict)))
+        _marshal = m
+    return _marshal
 
 
-def _rows(t: torch.Tensor | None, dtype, shape, dev: int, where: str):
-    """Address of a [T, heads, D] tensor whose rows may be further apart than one row."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not (
-            t.numel() == 0 or (t.stride(2) == 1 and t.stride(1) == shape[2])):
-        raise RptqError(RPTQ_ERR_INVALID_ARG, where)
-    return t.data_ptr()
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _paged(pages: torch.Tensor, page_table: torch.Tensor, bits: int, where: str):
-    """(device index, H, D, B, max_pages, n_pages, page_size) of a pool and its page table."""
-    dev = pages.get_device()
-    _need(pages.dim() == 4 and page_table.dim() == 2 and dev >= 0 and dev == torch._C._cuda_getDevice(), where)
-    n_pages, H, P, rb = pages.shape
-    _need(bits > 0 and rb * 8 % bits == 0, where)
-    B, max_pages = page_table.shape
-    return dev, H, rb * 8 // bits, B, max_pages, n_pages, P
-
-
-def _clusters(cluster, scale, zero, C: int, dev: int, where: str):
-    """Addresses of one tensor's (cluster, scale, zero) and its cluster count."""
-    g = scale.numel()
-    return (_arg(cluster, torch.int32, (C,), dev, where), _arg(scale, torch.float32, (g,), dev, where),
-            _arg(zero, torch.int32, (g,), dev, where)), g
-
-
-def _stream_handle(stream) -> int:
-    """The raw handle of a stream (the current stream of the current device without one)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+def _handle(stream):
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 def rptq_kv_paged_append(k_new, v_new, start, lens, page_table, k_pages, v_pages, cluster_k, scale_k, zero_k, cluster_v,
@@ -439,29 +415,10 @@ def rptq_kv_paged_append(k_new, v_new, start, lens, page_table, k_pages, v_pages
     """Quantize a ragged batch of new tokens [T, H, D] (either may be None; rows may be slices of a
     wider tensor) into the pages at the end of their sequences, in place; `weights`' new positions
     become 0."""
-    w = "rptq_kv_paged_append"
-    x, pool = (k_new, k_pages) if k_new is not None else (v_new, v_pages)
-    _need(x is not None and pool is not None and x.dtype in _DT, w)
-    dev, H, D, B, max_pages, n_pages, P = _paged(pool, page_table, bits, w)
-    T = x.shape[0]
-    ck, cv, g = (None,) * 3, (None,) * 3, set()
-    if k_new is not None:
-        ck, n = _clusters(cluster_k, scale_k, zero_k, H * D, dev, w)
-        g.add(n)
-    if v_new is not None:
-        cv, n = _clusters(cluster_v, scale_v, zero_v, H * D, dev, w)
-        g.add(n)
-    _need(len(g) == 1, w)
-    if k_new is not None and v_new is not None:
-        _need(T < 2 or k_new.stride(0) == v_new.stride(0), w)
-    st = lib().rptq_kv_paged_append(
-        _rows(k_new, x.dtype, (T, H, D), dev, w), _rows(v_new, x.dtype, (T, H, D), dev, w), _DT[x.dtype], T, H, D,
-        _row_stride(x), _arg(start, torch.int32, (B + 1,), dev, w), _arg(lens, torch.int32, (B,), dev, w), B,
-        _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages, P, *ck, *cv, g.pop(), bits,
-        _arg(k_pages, torch.uint8, pool.shape, dev, w) if k_new is not None else None,
-        _arg(v_pages, torch.uint8, pool.shape, dev, w) if v_new is not None else None,
-        _arg(weights, torch.float32, (n_pages, H, P), dev, w), _stream_handle(stream))
-    _check(st, w)
+    st = (_marshal or _paged()).append(k_new, v_new, start, lens, page_table, k_pages, v_pages, cluster_k, scale_k, zero_k,
+                                       cluster_v, scale_v, zero_v, bits, weights, _handle(stream))
+    if st:
+        raise RptqError(st, "rptq_kv_paged_append")
     return k_pages, v_pages
 
 
@@ -469,19 +426,10 @@ def rptq_kv_paged_dequant(pages, page_table, start, begin, cluster, scale, zero,
                           out_dtype=torch.float32, stream=None):
     """Positions begin[b] + i of sequence b read back into row start[b] + i of [T, H, D].  T: the rows
     (a host value; without it, out's)."""
-    w = "rptq_kv_paged_dequant"
-    dev, H, D, B, max_pages, n_pages, P = _paged(pages, page_table, bits, w)
-    if out is None:
-        _need(T is not None, w)
-        out = torch.empty((T, H, D), dtype=out_dtype, device=pages.device)
-    _need(out.dtype in _DT, w)
-    cl, g = _clusters(cluster, scale, zero, H * D, dev, w)
-    T = out.shape[0]
-    st = lib().rptq_kv_paged_dequant(
-        _arg(pages, torch.uint8, pages.shape, dev, w), H, D, bits, _arg(start, torch.int32, (B + 1,), dev, w),
-        _arg(begin, torch.int32, (B,), dev, w), B, _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages,
-        P, T, *cl, g, _arg(out, out.dtype, (T, H, D), dev, w), _DT[out.dtype], _stream_handle(stream))
-    _check(st, w)
+    st, out = (_marshal or _paged()).dequant(pages, page_table, start, begin, cluster, scale, zero, bits, -1 if T is None else T,
+                                             out, _DT.get(out_dtype, -1), _handle(stream))
+    if st:
+        raise RptqError(st, "rptq_kv_paged_dequant")
     return out
 
 
@@ -496,31 +444,11 @@ def rptq_kv_paged_attention(q, start, lens, page_table, k_pages, v_pages, cluste
     """Causal attention of each sequence's newest tokens q [T, Hq, D] (rows may be slices of a wider
     tensor) over all its positions; `weights` [n_pages, H, P], where given, grows by the positions'
     attention weights."""
-    w = "rptq_kv_paged_attention"
-    dev, H, D, B, max_pages, n_pages, P = _paged(k_pages, page_table, bits, w)
-    _need(q.dtype in _DT and q.dim() == 3, w)
-    T, Hq, _ = q.shape
-    dt = _DT[q.dtype]
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    L = lib()
-    ws_bytes = L.rptq_kv_paged_attention_workspace_size(T, Hq, H, D, dt, B, max_q, max_len, weights is not None)
-    if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
-    elif workspace.numel() * workspace.element_size() < ws_bytes:
-        raise RptqError(RPTQ_ERR_WORKSPACE, w)
-    ck, g = _clusters(cluster_k, scale_k, zero_k, H * D, dev, w)
-    cv, gv = _clusters(cluster_v, scale_v, zero_v, H * D, dev, w)
-    _need(g == gv, w)
-    st = L.rptq_kv_paged_attention(
-        _rows(q, q.dtype, (T, Hq, D), dev, w), dt, T, Hq, H, D, _row_stride(q),
-        _arg(start, torch.int32, (B + 1,), dev, w), _arg(lens, torch.int32, (B,), dev, w), B, max_q, max_len,
-        _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages, P,
-        _arg(k_pages, torch.uint8, k_pages.shape, dev, w), _arg(v_pages, torch.uint8, k_pages.shape, dev, w), *ck, *cv, g, bits,
-        float(scale), _arg(out, q.dtype, (T, Hq, D), dev, w), _arg(weights, torch.float32, (n_pages, H, P), dev, w),
-        None if workspace is None else _arg(workspace, workspace.dtype, workspace.shape, dev, w),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    _check(st, w)
+    st, out = (_marshal or _paged()).attention(q, start, lens, page_table, k_pages, v_pages, cluster_k, scale_k, zero_k,
+                                               cluster_v, scale_v, zero_v, bits, max_q, max_len, scale, out, weights,
+                                               workspace, _handle(stream))
+    if st:
+        raise RptqError(st, "rptq_kv_paged_attention")
     return out
 
 
@@ -528,19 +456,10 @@ def rptq_kv_paged_evict(k_pages, v_pages, weights, lens, page_table, bits: int, 
                         max_len: int | None = None, new_lens=None, kept=None, stream=None):
     """Cut every (sequence, head) to `budget` positions: the last `recent` and those of the largest
     running sums, moved together in place.  Returns (new_lens [B], kept [B, H, budget])."""
-    w = "rptq_kv_paged_evict"
-    dev, H, D, B, max_pages, n_pages, P = _paged(k_pages, page_table, bits, w)
-    if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=lens.device)
-    if kept is None:
-        kept = torch.empty((B, H, max(budget, 0)), dtype=torch.int32, device=lens.device)
-    st = lib().rptq_kv_paged_evict(
-        _arg(k_pages, torch.uint8, k_pages.shape, dev, w), _arg(v_pages, torch.uint8, k_pages.shape, dev, w),
-        _arg(weights, torch.float32, (n_pages, H, P), dev, w), B, H, D, bits, _arg(lens, torch.int32, (B,), dev, w),
-        _arg(page_table, torch.int32, (B, max_pages), dev, w), max_pages, n_pages, P,
-        max_pages * P if max_len is None else max_len, budget, recent, _arg(new_lens, torch.int32, (B,), dev, w),
-        _arg(kept, torch.int32, (B, H, max(budget, 0)), dev, w), _stream_handle(stream))
-    _check(st, w)
+    st, new_lens, kept = (_marshal or _paged()).evict(k_pages, v_pages, weights, lens, page_table, bits, budget, recent,
+                                                      -1 if max_len is None else max_len, new_lens, kept, _handle(stream))
+    if st:
+        raise RptqError(st, "rptq_kv_paged_evict")
     return new_lens, kept
 
 
