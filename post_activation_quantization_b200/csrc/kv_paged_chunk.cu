@@ -6,7 +6,7 @@
 // 128; all 512 tensor-memory columns: S of both tiles (W replaces it in place, as fp16) and O of both.
 //   warps 0-3, 4-7    softmax of tile 0 / 1: one thread to a row
 //   warps 8-11        expand the packed codes of K and V into shared memory, as fp16
-//   warps 12, 13      issue the MMAs of tile 0 / 1
+//   warp 12           issues the MMAs of both
 // The two tiles share K and V and take turns on the tensor core: one's softmax runs while the other's
 // products do.  The codes come from global memory a tile ahead, are masked in place (kv_paged_attn.cuh) and
 // brought to small exact fp16 numbers by one fused multiply-add per two: K's relative to position 0's codes (a shift of all
@@ -28,7 +28,7 @@ namespace rptq {
 constexpr int CH_M = 128, CH_KEYS = 128;
 constexpr int CH_SOFT_WARPS = 8, CH_PROD_WARPS = 4;
 constexpr int CH_PROD0 = CH_SOFT_WARPS, CH_MMA0 = CH_PROD0 + CH_PROD_WARPS;
-constexpr int CH_THREADS = 32 * (CH_MMA0 + 2);
+constexpr int CH_THREADS = 32 * (CH_MMA0 + 1);
 constexpr uint32_t CH_SLAB = CH_M * 128;  // 128 rows of 64 fp16
 // Weights are held as 2^y, y = x - m + CH_PSHIFT for a reference m that follows the running maximum (it moves when
 // some y passes CH_YMAX); fp16's smallest step is then 2^-(24 + CH_PSHIFT) of a weight at the reference.
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     using KP = KPairs<BITS, D>;
     constexpr int ST = S::STAGES;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[4 * 2 + 3 * 2 + 1 + 2];
+    __shared__ __align__(8) uint64_t bars[4 * 2 + 3 * 2 + 2];
     __shared__ uint32_t tmem_slot;
     __shared__ float s_sv[D], s_zv[D];
     const PagedAttnDev &a = c.a;
@@ -266,14 +266,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(k_full + 8 * i, 32 * CH_PROD_WARPS);
             mbar_init(v_full + 8 * i, 32 * CH_PROD_WARPS);
-            mbar_init(k_empty + 8 * i, nact);
-            mbar_init(v_empty + 8 * i, nact);
+            mbar_init(k_empty + 8 * i, 1);
+            mbar_init(v_empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, CH_M);
             mbar_init(o_done + 8 * i, 1);
-            mbar_init(drain + 8 * i, 1);
         }
         mbar_init(q_full, 1);
+        mbar_init(drain, 1);
         fence_mbar_init();
     }
     for (int d = tid; d < D; d += CH_THREADS) {
@@ -468,41 +468,53 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         }
         if (pt == 0) mbar_wait_bounded(q_full, 0, p.err);  // no copy may be in flight when the CTA ends
     } else {
-        const int g = warp - CH_MMA0;
-        if (lane == 0 && g < nact) {
+        // ---- MMA issue: the tiles in turn, each its W V of this turn and then its q' K^T of the next, so that one
+        //      tile's products run during the other's softmax ----
+        if (lane == 0) {
             constexpr uint32_t qk = f16_idesc(CH_M, CH_KEYS), pv = f16_idesc(CH_M, D) | IDESC_B_MN;
-            const uint32_t tS = tmem + (uint32_t)g * CH_KEYS, tO = tmem + S::O_COL + (uint32_t)g * D;
-            const uint32_t q0 = sQ + g * S::QT;
-            bool ok = mbar_wait_bounded(q_full, 0, p.err);
-            for (int j = j0; j < j1 && ok; ++j) {
-                const int i = j - j0, st = i % ST;
-                const uint32_t ph = (uint32_t)(i / ST) & 1;
-                // S (and W in its place) is free once the products that read it are complete
-                if (i > 0 && !(ok = mbar_wait_bounded(o_done + 8 * g, (i - 1) & 1, p.err))) break;
-                if (!(ok = mbar_wait_bounded(k_full + 8 * st, ph, p.err))) break;
-                tc_fence_after();
+            const int count = j1 - j0;
+            auto scores = [&](int g, int st) {
+                const uint32_t q0 = sQ + g * S::QT;
 #pragma unroll
                 for (int part = 0; part < QP; ++part)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        tc_mma_f16_ss(tS, sw128_desc(q0 + (part * S::SLABS + kk / 4) * CH_SLAB) + 2 * (kk % 4),
+                        tc_mma_f16_ss(tmem + (uint32_t)g * CH_KEYS, sw128_desc(q0 + (part * S::SLABS + kk / 4) * CH_SLAB) + 2 * (kk % 4),
                                       sw128_desc(sK + st * S::KV + kk / 4 * CH_SLAB) + 2 * (kk % 4), qk, (part | kk) != 0);
-                tc_commit(k_empty + 8 * st);
                 tc_commit(s_full + 8 * g);
-                if (!(ok = mbar_wait_bounded(p_full + 8 * g, i & 1, p.err))) break;
-                if (!(ok = mbar_wait_bounded(v_full + 8 * st, ph, p.err))) break;
+            };
+            bool ok = mbar_wait_bounded(q_full, 0, p.err);
+            if (ok && count > 0 && (ok = mbar_wait_bounded(k_full, 0, p.err))) {
                 tc_fence_after();
-#pragma unroll
-                for (int part = 0; part < PP; ++part)
-#pragma unroll
-                    for (int kk = 0; kk < CH_KEYS / 16; ++kk)
-                        tc_mma_f16_ts(tO, tS + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part,
-                                      sw128_mn_desc(sV + st * S::KV + kk * 2048, CH_SLAB), pv, i > 0 || (part | kk) != 0);
-                tc_commit(v_empty + 8 * st);
-                tc_commit(o_done + 8 * g);
+                for (int g = 0; g < nact; ++g) scores(g, 0);
+                tc_commit(k_empty);
             }
-            tc_commit(drain + 8 * g);  // tensor memory is released below: every issued product first
-            mbar_wait_bounded(drain + 8 * g, 0, p.err);
+            for (int i = 0; i < count && ok; ++i) {
+                const int st = i % ST, st1 = (i + 1) % ST;
+                for (int g = 0; g < nact && ok; ++g) {
+                    const uint32_t tS = tmem + (uint32_t)g * CH_KEYS, tO = tmem + S::O_COL + (uint32_t)g * D;
+                    if (!(ok = mbar_wait_bounded(p_full + 8 * g, i & 1, p.err))) break;
+                    if (!(ok = mbar_wait_bounded(v_full + 8 * st, (uint32_t)(i / ST) & 1, p.err))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int part = 0; part < PP; ++part)
+#pragma unroll
+                        for (int kk = 0; kk < CH_KEYS / 16; ++kk)
+                            tc_mma_f16_ts(tO, tS + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part,
+                                          sw128_mn_desc(sV + st * S::KV + kk * 2048, CH_SLAB), pv, i > 0 || (part | kk) != 0);
+                    if (g == nact - 1) tc_commit(v_empty + 8 * st);
+                    tc_commit(o_done + 8 * g);
+                    if (i + 1 == count) continue;
+                    if (!(ok = mbar_wait_bounded(k_full + 8 * st1, (uint32_t)((i + 1) / ST) & 1, p.err))) break;
+                    // S (and W in its place) is free once the products that read it are complete
+                    if (!(ok = mbar_wait_bounded(o_done + 8 * g, i & 1, p.err))) break;
+                    tc_fence_after();
+                    scores(g, st1);
+                    if (g == nact - 1) tc_commit(k_empty + 8 * st1);
+                }
+            }
+            tc_commit(drain);  // tensor memory is released below: every issued product first
+            mbar_wait_bounded(drain, 0, p.err);
         }
         __syncwarp();
     }
