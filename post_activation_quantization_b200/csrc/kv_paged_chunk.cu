@@ -6,7 +6,7 @@
 // 128; all 512 tensor-memory columns: S of both tiles (W replaces it in place, as fp16) and O of both.
 //   warps 0-3, 4-7    softmax of tile 0 / 1: one thread to a row
 //   warps 8-11        expand the packed codes of K and V into shared memory, as fp16
-//   warp 12           issues the MMAs of both
+//   warp 12           issues the MMAs of both (warps 13-15 fill its warpgroup)
 // The two tiles share K and V and take turns on the tensor core: one's softmax runs while the other's
 // products do.  The codes come from global memory a tile ahead, are masked in place (kv_paged_attn.cuh) and
 // brought to small exact fp16 numbers by one fused multiply-add per two: K's relative to position 0's codes (a shift of all
@@ -28,7 +28,7 @@ namespace rptq {
 constexpr int CH_M = 128, CH_KEYS = 128;
 constexpr int CH_SOFT_WARPS = 8, CH_PROD_WARPS = 4;
 constexpr int CH_PROD0 = CH_SOFT_WARPS, CH_MMA0 = CH_PROD0 + CH_PROD_WARPS;
-constexpr int CH_THREADS = 32 * (CH_MMA0 + 1);
+constexpr int CH_THREADS = 32 * (CH_MMA0 + 4);  // whole warpgroups: registers are moved between them
 constexpr uint32_t CH_SLAB = CH_M * 128;  // 128 rows of 64 fp16
 // Weights are held as 2^y, y = x - m + CH_PSHIFT for a reference m that follows the running maximum (it moves when
 // some y passes CH_YMAX); fp16's smallest step is then 2^-(24 + CH_PSHIFT) of a weight at the reference.
@@ -287,7 +287,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
+    // 512 threads start with 128 registers each; a row of S takes 128: 2 * 168 + 112 + 64 = 4 * 128
     if (warp < CH_SOFT_WARPS) {
+        reg_inc<168>();
         const int g = warp >> 2, quad = warp & 3;
         const int r = 32 * quad + lane, row = row0 + g * CH_M + r;  // the thread's row
         const bool live = g < nact && row < R;
@@ -307,19 +309,20 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 const int pos0 = j * CH_KEYS;
                 const bool whole = pos0 + CH_KEYS <= vmin;
                 float top = -INFINITY;
+                uint32_t v[4][32];  // the row of S
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    uint32_t v[32];
-                    tc_ld32(tS + 32 * q4, v);
-                    if (whole) {
+                for (int q4 = 0; q4 < 4; ++q4) tc_ld32_async(tS + 32 * q4, v[q4]);
+                tc_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; k += 2) top = max3f(top, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                    } else {
+                for (int q4 = 0; q4 < 4; ++q4) tc_loaded(v[q4]);
+                if (!whole) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (pos0 + 32 * q4 + k < vrow) top = fmaxf(top, __uint_as_float(v[k]));
-                    }
+                    for (int k = 0; k < CH_KEYS; ++k)
+                        if (pos0 + k >= vrow) v[k / 32][k % 32] = 0xff800000u;  // -inf (cx > 0)
                 }
+#pragma unroll
+                for (int k = 0; k < CH_KEYS; k += 2)
+                    top = max3f(top, __uint_as_float(v[k / 32][k % 32]), __uint_as_float(v[k / 32][k % 32 + 1]));
                 // cx > 0, so the largest score is cx * the largest S
                 const float ytop = fmaf(top, cx, off);
                 if (__any_sync(FULL, ytop > CH_YMAX)) {
@@ -333,27 +336,22 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                     }
                     if (j > j0) {  // O of the tiles so far (its products are complete: the scores waited for them)
 #pragma unroll 1
-                        for (int q4 = 0; q4 < D / 32; ++q4) {
-                            uint32_t v[32];
-                            tc_ld32(tO + 32 * q4, v);
+                        for (int q8 = 0; q8 < D / 8; ++q8) {
+                            uint32_t x[8];
+                            tc_ld8(tO + 8 * q8, x);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-                            tc_st32(tO + 32 * q4, v);
+                            for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+                            tc_st8(tO + 8 * q8, x);
                         }
                     }
                 }
                 const f32x2 cx2 = mk2(cx, cx), off2 = mk2(off, off);
 #pragma unroll
                 for (int q4 = 0; q4 < 4; ++q4) {
-                    uint32_t v[32], w[16], w2[16];
-                    tc_ld32(tS + 32 * q4, v);
+                    uint32_t w[16], w2[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        f32x2 y = fma2(mk2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), cx2, off2);
-                        if (!whole) {
-                            const int pos = pos0 + 32 * q4 + 2 * k;
-                            y = mk2(pos < vrow ? lo2(y) : -INFINITY, pos + 1 < vrow ? hi2(y) : -INFINITY);
-                        }
+                        const f32x2 y = fma2(mk2(__uint_as_float(v[q4][2 * k]), __uint_as_float(v[q4][2 * k + 1])), cx2, off2);
                         const f32x2 e = mk2(ex2(lo2(y)), ex2(hi2(y)));
                         l2 = add2(l2, e);
                         w[k] = half2_bits(lo2(e), hi2(e));
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                             w2[k] = half2_bits(lo2(e) - hf.x, hi2(e) - hf.y);
                         }
                     }
-                    // W over the 32 columns of S just read: 16 columns, its second part in the next 16
+                    // W over 32 columns of S: 16 columns, its second part in the next 16
                     tc_st16(tS + 32 * q4, w);
                     if (PP == 2) tc_st16(tS + 32 * q4 + 16, w2);
                 }
@@ -433,6 +431,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         }
     } else if (warp < CH_MMA0) {
         // ---- producers ----
+        reg_dec<112>();
         const int pt = tid - 32 * CH_PROD0;
         if (pt == 0) {
             const uint8_t *src = c.tiles + qslot * S::QT;
@@ -470,7 +469,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     } else {
         // ---- MMA issue: the tiles in turn, each its W V of this turn and then its q' K^T of the next, so that one
         //      tile's products run during the other's softmax ----
-        if (lane == 0) {
+        reg_dec<64>();
+        if (warp == CH_MMA0 && lane == 0) {
             constexpr uint32_t qk = f16_idesc(CH_M, CH_KEYS), pv = f16_idesc(CH_M, D) | IDESC_B_MN;
             const int count = j1 - j0;
             auto scores = [&](int g, int st) {
