@@ -34,6 +34,23 @@ constexpr uint32_t CH_SLAB = CH_M * 128;  // 128 rows of 64 fp16
 // some y passes CH_YMAX); fp16's smallest step is then 2^-(24 + CH_PSHIFT) of a weight at the reference.
 constexpr float CH_PSHIFT = 5.f, CH_YMAX = 15.f;
 
+// 2^y of two exponents on the FMA pipe: y = n + f with n the nearest integer (the sum with 1.5 * 2^23 holds it in its
+// low bits), 2^f on [-1/2, 1/2] by the cubic of least relative error (7.5e-5, fitted for this; a weight's fp16 rounding
+// is up to 4.9e-4), n added to the exponent.  y below -126 counts as -126.  The special-function unit gives 16 results a clock
+// and SM, which the tensor core's two products of a tile take no longer than: one weight in CH_POLY comes from here.
+__device__ __forceinline__ f32x2 exp2_poly(f32x2 y)
+{
+    y = mk2(fmaxf(lo2(y), -126.f), fmaxf(hi2(y), -126.f));
+    const f32x2 t = add2(y, mk2(MAGIC_RINT, MAGIC_RINT));
+    const f32x2 f = fma2(add2(t, mk2(-MAGIC_RINT, -MAGIC_RINT)), mk2(-1.f, -1.f), y);
+    f32x2 p = fma2(f, mk2(0.05517167f, 0.05517167f), mk2(0.24261112f, 0.24261112f));
+    p = fma2(p, f, mk2(0.69326099f, 0.69326099f));
+    p = fma2(p, f, mk2(0.99992807f, 0.99992807f));
+    return mk2(__uint_as_float(__float_as_uint(lo2(t)) * 0x800000u + __float_as_uint(lo2(p))),
+               __uint_as_float(__float_as_uint(hi2(t)) * 0x800000u + __float_as_uint(hi2(p))));
+}
+constexpr int CH_POLY = 8;  // (measured at 2048 tokens, 32 heads: none 537 us, 1 in 8 517, 1 in 4 550, 1 in 2 589)
+
 // What the chunk kernels read besides PagedAttnDev.
 struct ChunkDev {
     PagedAttnDev a;
@@ -77,6 +94,36 @@ struct ChunkQ {
     }
 };
 
+// N consecutive elements (2 or 4, aligned to their size) of a tensor of run-time type
+template <int N>
+__device__ __forceinline__ void load_row(const void *p, int dtype, int64_t at, float (&v)[N])
+{
+    if (dtype == RPTQ_F32) {
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+            const float2 f = *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + at + k);
+            v[k] = f.x, v[k + 1] = f.y;
+        }
+        return;
+    }
+    uint32_t w[N / 2];
+    if constexpr (N == 4) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at);
+        w[0] = u.x, w[1] = u.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + at);
+    }
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+        if (dtype == RPTQ_F16) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+            v[2 * k] = f.x, v[2 * k + 1] = f.y;
+        } else {
+            v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+    }
+}
+
 // ---- the queries as operand tiles -----------------------------------------------------------------------
 // One CTA per (tile slot, head), a warp to a row.  PARTS = 1: fp16 of q' scaled so that the row's largest is in
 // [2^14, 2^15); 2: integers of 11 bits, the second 2^-11 of the first's unit and stored so.
@@ -89,7 +136,8 @@ __global__ void __launch_bounds__(CQ_THREADS)
     constexpr uint32_t BYTES = PARTS * (D / 64) * CH_SLAB;
     extern __shared__ __align__(16) uint8_t tile[];
     __shared__ float s_s[D];
-    __shared__ int s_at[D];  // byte of channel d in a row of the tile (before the swizzle), pos << 16
+    __shared__ uint32_t s_at[D];  // byte of channel d in a row of the tile (before the swizzle)
+    __shared__ float s_down[D];   // 2^-pos of its code
     const PagedAttnDev &a = c.a;
     const Paged &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -105,38 +153,55 @@ __global__ void __launch_bounds__(CQ_THREADS)
         int col, pos;
         ChunkQ<BITS, D>::column(d, col, pos);
         s_s[d] = a.kt.sk[cluster_of(a.kt.ck, h * D + d, a.kt.g, p.err)];
-        s_at[d] = (col >> 6) * CH_SLAB + (col & 63) * 2 | pos << 24;
+        s_at[d] = (col >> 6) * CH_SLAB + (col & 63) * 2;
+        s_down[d] = 1.f / (float)(1 << pos);
     }
     __syncthreads();
-    for (int r = warp; r < CH_M; r += CQ_THREADS / 32) {
-        const int64_t row = i * CH_M + r;
-        const int tok = (int)(row / a.G), j = (int)(row - (int64_t)tok * a.G);
-        float v[CPL], m = 0.f;
+    // four rows of a warp at a time, their loads together
+    constexpr int U = 4, W = CQ_THREADS / 32;
+    for (int r0 = warp * U; r0 < CH_M; r0 += W * U) {
+        float v[U][CPL], m[U];
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) {
-            const int d = lane * CPL + k;
-            v[k] = r < rows ? load_elem(a.q, a.dtype, (int64_t)(s0 + tok) * a.q_stride + (int64_t)(h * a.G + j) * D + d) * s_s[d] : 0.f;
-            m = fmaxf(m, fabsf(v[k]));
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = i * CH_M + r0 + u;
+            const int tok = (int)(row / a.G), j = (int)(row - (int64_t)tok * a.G);
+            const int64_t at = (int64_t)(s0 + tok) * a.q_stride + (int64_t)(h * a.G + j) * D + lane * CPL;
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) v[u][k] = 0.f;
+            if (r0 + u < rows) load_row<CPL>(a.q, a.dtype, at, v[u]);
         }
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-        int ex = 0;
-        if (m > 0.f && m < INFINITY) frexpf(m, &ex);
-        ex = max(ex, -100);
-        const int grid = PARTS == 1 ? 15 : 11;
-        const float up = ldexpf(1.f, grid - ex);
-        if (lane == 0) c.cx[((int64_t)h * c.slots + slot) * CH_M + r] = ldexpf(a.scale * LOG2E, ex - grid + 10);
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) {
-            const int at = s_at[lane * CPL + k], pos = at >> 24;
-            const uint32_t o = (uint32_t)(at & 0xFFFFFF) + r * 128;
-            const uint32_t sw = o ^ ((r & 7) << 4);  // 16-byte piece c of a row sits at c ^ (row mod 8)
-            const float down = __uint_as_float((uint32_t)(127 - pos) << 23);  // 2^-pos
-            float f = v[k] * up;
-            const float g = PARTS == 1 ? f : rintf(f);
-            *reinterpret_cast<__half *>(tile + sw) = __float2half_rn(g * down);
-            if (PARTS == 2) {  // on the grid of 2^-11: exact in fp16
-                f = rintf((f - g) * 2048.f) * 0x1p-11f;
-                *reinterpret_cast<__half *>(tile + (D / 64) * CH_SLAB + sw) = __float2half_rn(f * down);
+        for (int u = 0; u < U; ++u) {
+            m[u] = 0.f;
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                v[u][k] *= s_s[lane * CPL + k];
+                m[u] = fmaxf(m[u], fabsf(v[u][k]));
+            }
+        }
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(FULL, m[u], o));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u;
+            int ex = 0;
+            if (m[u] > 0.f && m[u] < INFINITY) frexpf(m[u], &ex);
+            ex = max(ex, -100);
+            const int grid = PARTS == 1 ? 15 : 11;
+            const float up = __uint_as_float((uint32_t)(127 + grid - ex) << 23);  // 2^(grid - ex): grid - ex <= 115
+            if (lane == 0) c.cx[((int64_t)h * c.slots + slot) * CH_M + r] = ldexpf(a.scale * LOG2E, ex - grid + 10);
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                const uint32_t sw = (s_at[lane * CPL + k] + r * 128) ^ ((r & 7) << 4);  // piece c of a row sits at c ^ (row mod 8)
+                const float down = s_down[lane * CPL + k];
+                float f = v[u][k] * up;
+                const float g = PARTS == 1 ? f : rintf(f);
+                *reinterpret_cast<__half *>(tile + sw) = __float2half_rn(g * down);
+                if (PARTS == 2) {  // on the grid of 2^-11: exact in fp16
+                    f = rintf((f - g) * 2048.f) * 0x1p-11f;
+                    *reinterpret_cast<__half *>(tile + (D / 64) * CH_SLAB + sw) = __float2half_rn(f * down);
+                }
             }
         }
     }
@@ -157,13 +222,32 @@ __device__ __forceinline__ void chunk_share(int pt, int &r0, int &t)
     else
         t = pt & 3, r0 = pt >> 2;
 }
+// The pages of its four rows of the tile at pos0, as the table has them; page 0 for one outside the pool.
+__device__ __forceinline__ void chunk_pages(const Paged &p, int b, int pos0, int L, int r0, int (&ids)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int pos = pos0 + r0 + 32 * i;
+        ids[i] = pos < L ? p.table[(int64_t)b * p.max_pages + (pos >> p.shift)] : 0;
+    }
+}
+__device__ __forceinline__ void chunk_check(const Paged &p, int (&ids)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (ids[i] < 0 || ids[i] >= p.n_pages) {
+            raise_error(p.err, RPTQ_DEVERR_PAGE);
+            ids[i] = 0;
+        }
+}
 // its four rows' packed words ...
 template <int BITS, int D>
 struct ChunkCodes {
     using KP = KPairs<BITS, D>;
     uint32_t w[4][KP::NW];
-    // rows r0, r0 + 32, ... of the tile at pos0; zeros past the sequence
-    __device__ __forceinline__ void read(const uint8_t *pages, const Paged &p, int b, int H, int h, int pos0, int L, int r0, int t)
+    // rows r0, r0 + 32, ... of the tile at pos0, in pages `ids`; zeros past the sequence
+    __device__ __forceinline__ void read(const uint8_t *pages, const Paged &p, const int (&ids)[4], int H, int h, int pos0, int L,
+                                         int r0, int t)
     {
         constexpr int RB = D * BITS / 8;
 #pragma unroll
@@ -171,10 +255,7 @@ struct ChunkCodes {
             const int pos = pos0 + r0 + 32 * i;
 #pragma unroll
             for (int k = 0; k < KP::NW; ++k) w[i][k] = 0;
-            if (pos < L) {
-                const int page = max(paged_page(p, b, pos >> p.shift), 0);
-                KP::read(pages + (paged_row(page, H, h, p.shift) + (pos & ((1 << p.shift) - 1))) * RB, t, w[i]);
-            }
+            if (pos < L) KP::read(pages + (paged_row(ids[i], H, h, p.shift) + (pos & ((1 << p.shift) - 1))) * RB, t, w[i]);
         }
     }
     // ... to shared memory: fp16 of D / 64 slabs of [128 rows, 128 bytes] in the 128-byte swizzle
@@ -352,7 +433,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const f32x2 y = fma2(mk2(__uint_as_float(v[q4][2 * k]), __uint_as_float(v[q4][2 * k + 1])), cx2, off2);
-                        const f32x2 e = mk2(ex2(lo2(y)), ex2(hi2(y)));
+                        // (exact sums of weights, QP = 2, stay with the finer function)
+                        const f32x2 e = QP == 1 && k % CH_POLY == CH_POLY - 1 ? exp2_poly(y) : mk2(ex2(lo2(y)), ex2(hi2(y)));
                         l2 = add2(l2, e);
                         w[k] = half2_bits(lo2(e), hi2(e));
                         if (PP == 2) {
@@ -445,8 +527,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             uint32_t ref[KP::N];
             chunk_reference<BITS, D>(a, b, h, t, ref);
             ChunkCodes<BITS, D> kc, vc;
-            kc.read(a.kq, p, b, a.H, h, j0 * CH_KEYS, L, r0, t);
-            vc.read(a.vq, p, b, a.H, h, j0 * CH_KEYS, L, r0, t);
+            int ids[4];  // pages of the tile whose codes are read next: themselves read a tile before that
+            chunk_pages(p, b, j0 * CH_KEYS, L, r0, ids);
+            chunk_check(p, ids);
+            kc.read(a.kq, p, ids, a.H, h, j0 * CH_KEYS, L, r0, t);
+            vc.read(a.vq, p, ids, a.H, h, j0 * CH_KEYS, L, r0, t);
+            chunk_pages(p, b, (j0 + 1) * CH_KEYS, L, r0, ids);
             for (int j = j0; j < j1 && ok; ++j) {
                 const int i = j - j0, st = i % ST;
                 const uint32_t free_ph = ((uint32_t)(i / ST) & 1) ^ 1;
@@ -457,12 +543,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 });
                 fence_proxy_async_smem();
                 lin_arrive(k_full + 8 * st);
-                if (j + 1 < j1) kc.read(a.kq, p, b, a.H, h, (j + 1) * CH_KEYS, L, r0, t);
+                chunk_check(p, ids);
+                if (j + 1 < j1) kc.read(a.kq, p, ids, a.H, h, (j + 1) * CH_KEYS, L, r0, t);
                 if (!(ok = mbar_wait_bounded(v_empty + 8 * st, free_ph, p.err))) break;
                 vc.write(sV + st * S::KV, r0, t, [&](uint32_t(&x)[KP::N]) { KP::about_mid(x); });
                 fence_proxy_async_smem();
                 lin_arrive(v_full + 8 * st);
-                if (j + 1 < j1) vc.read(a.vq, p, b, a.H, h, (j + 1) * CH_KEYS, L, r0, t);
+                if (j + 1 < j1) vc.read(a.vq, p, ids, a.H, h, (j + 1) * CH_KEYS, L, r0, t);
+                chunk_pages(p, b, (j + 2) * CH_KEYS, L, r0, ids);
             }
         }
         if (pt == 0) mbar_wait_bounded(q_full, 0, p.err);  // no copy may be in flight when the CTA ends
@@ -494,7 +582,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 for (int g = 0; g < nact && ok; ++g) {
                     const uint32_t tS = tmem + (uint32_t)g * CH_KEYS, tO = tmem + S::O_COL + (uint32_t)g * D;
                     if (!(ok = mbar_wait_bounded(p_full + 8 * g, i & 1, p.err))) break;
-                    if (!(ok = mbar_wait_bounded(v_full + 8 * st, (uint32_t)(i / ST) & 1, p.err))) break;
+                    if (g == 0 && !(ok = mbar_wait_bounded(v_full + 8 * st, (uint32_t)(i / ST) & 1, p.err))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int part = 0; part < PP; ++part)
@@ -502,10 +590,10 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                         for (int kk = 0; kk < CH_KEYS / 16; ++kk)
                             tc_mma_f16_ts(tO, tS + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part,
                                           sw128_mn_desc(sV + st * S::KV + kk * 2048, CH_SLAB), pv, i > 0 || (part | kk) != 0);
-                    if (g == nact - 1) tc_commit(v_empty + 8 * st);
                     tc_commit(o_done + 8 * g);
+                    if (g == nact - 1) tc_commit(v_empty + 8 * st);
                     if (i + 1 == count) continue;
-                    if (!(ok = mbar_wait_bounded(k_full + 8 * st1, (uint32_t)((i + 1) / ST) & 1, p.err))) break;
+                    if (g == 0 && !(ok = mbar_wait_bounded(k_full + 8 * st1, (uint32_t)((i + 1) / ST) & 1, p.err))) break;
                     // S (and W in its place) is free once the products that read it are complete
                     if (!(ok = mbar_wait_bounded(o_done + 8 * g, i & 1, p.err))) break;
                     tc_fence_after();
@@ -577,7 +665,10 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         uint32_t ref[KP::N];
         chunk_reference<BITS, D>(a, b, h, t, ref);
         ChunkCodes<BITS, D> kc;
-        kc.read(a.kq, p, b, a.H, h, pos0, L, r0, t);
+        int ids[4];
+        chunk_pages(p, b, pos0, L, r0, ids);
+        chunk_check(p, ids);
+        kc.read(a.kq, p, ids, a.H, h, pos0, L, r0, t);
         kc.write(sK, r0, t, [&](uint32_t(&x)[KP::N]) {
 #pragma unroll
             for (int k = 0; k < KP::N; ++k) x[k] = code_up_plus(x[k], ref[k]);
