@@ -19,7 +19,7 @@ namespace rptq {
 // byte once and are bound by HBM at large batches and by the launch at small ones.
 constexpr int PG_THREADS = 256;
 constexpr int PG_ROWS = 64;  // most rows of a CTA's chunk
-constexpr int PG_UNROLL = 4;  // rows whose loads are in flight together
+constexpr int PG_UNROLL = 4;  // 16-byte loads (words, for the read-back) of a step, the next step's issued before it
 
 // Four lanes' 24-bit groups <-> the three 32-bit words they fill (lane j of the four holds word j < 3).
 __device__ __forceinline__ uint32_t pack_a3_words(uint32_t grp, int lane)
@@ -33,17 +33,18 @@ __device__ __forceinline__ uint32_t unpack_a3_words(uint32_t w, int lane)
     const int j = lane & 3, base = lane & ~3;
     const uint32_t lo = __shfl_sync(FULL, w, base + (j == 3 ? 2 : max(j - 1, 0)));
     const uint32_t hi = __shfl_sync(FULL, w, base + min(j, 2));
-    // group j is bits 24j .. 24j + 23 of the 96: words (0), (0, 1), (1, 2), (2)
-    return j == 0 ? lo : j == 3 ? lo >> 8 : __funnelshift_r(lo, hi, 32 - 8 * j);
+    // group j is bits 24j .. 24j + 23 of the 96: words (0), (0, 1), (1, 2), (2); what is above its 24 bits is not its own
+    return __funnelshift_r(lo, hi, (32 - 8 * j) & 31);
 }
 
 template <typename T, int BITS>
-__global__ void __launch_bounds__(PG_THREADS)
+__global__ void __launch_bounds__(PG_THREADS, 2)
     kv_paged_append_kernel(KvTensors t, Paged p, int64_t row_stride, int H, int D, int g, int rows_per_cta,
                            float *__restrict__ weights)
 {
     constexpr int VEC = Elem<T>::VEC, NLD = 8 / VEC;
-    __shared__ int s_page[PG_ROWS], s_slot[PG_ROWS];
+    constexpr int U = PG_UNROLL / NLD;  // rows of a step
+    __shared__ int64_t s_row[PG_ROWS];  // byte of head 0's row of each position; -1: none
     const int tid = threadIdx.x, lane = tid & 31;
     const T *src = static_cast<const T *>(t.src[blockIdx.z]);
     if (src == nullptr) return;
@@ -61,8 +62,7 @@ __global__ void __launch_bounds__(PG_THREADS)
                 slot = pos & ((1 << p.shift) - 1);
             }
         }
-        s_page[tid] = page;
-        s_slot[tid] = slot;
+        s_row[tid] = page < 0 ? -1 : (paged_row(page, H, 0, p.shift) + slot) * (D * BITS / 8);
     }
     const int c0 = (blockIdx.y * blockDim.x + tid) * 8;
     const bool live = c0 < H * D;
@@ -71,27 +71,39 @@ __global__ void __launch_bounds__(PG_THREADS)
     cf.load(t.cl[blockIdx.z], t.sc[blockIdx.z], t.zp[blockIdx.z], c, g, p.err);
     __syncthreads();
     const int rb = D * BITS / 8;
-    for (int i0 = 0; i0 < rows; i0 += PG_UNROLL) {
-        uint4 x[PG_UNROLL][NLD];
+    const T *col = src + t0 * row_stride + c;  // of the next rows to load
+    // the thread's word of a row; of the four lanes that share 96 bits, three store
+    const bool mine = live && (BITS == 4 || (lane & 3) < 3);
+    uint8_t *word = dst + ((int64_t)h << p.shift) * rb + (BITS == 4 ? d0 / 2 : (d0 & ~31) * 3 / 8 + (lane & 3) * 4);
+    const bool zeroes = weights != nullptr && blockIdx.z == 0 && live && d0 == 0;
+    uint4 x[U][NLD];  // the next U rows, loaded while the U before them are quantized
+    auto load = [&](int i0) {
 #pragma unroll
-        for (int u = 0; u < PG_UNROLL; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int l = 0; l < NLD; ++l)
-                x[u][l] = i0 + u < rows ? ldg_stream(src + (t0 + i0 + u) * row_stride + c + l * VEC) : make_uint4(0, 0, 0, 0);
+                x[u][l] = i0 + u < rows ? ldg_stream(col + u * row_stride + l * VEC) : make_uint4(0, 0, 0, 0);
+        col += U * row_stride;
+    };
+    load(0);
+    for (int i0 = 0; i0 < rows; i0 += U) {
+        uint4 y[U][NLD];
 #pragma unroll
-        for (int u = 0; u < PG_UNROLL; ++u) {
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int l = 0; l < NLD; ++l) y[u][l] = x[u][l];
+        if (i0 + U < rows) load(i0 + U);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             const int i = i0 + u;
             if (i >= rows) break;
             uint32_t grp[1];
-            kv_quant_row<T, BITS, 8>(x[u], cf, grp);
+            kv_quant_row<T, BITS, 8>(y[u], cf, grp);
             const uint32_t w = BITS == 4 ? grp[0] : pack_a3_words(grp[0], lane);
-            if (!live || s_page[i] < 0) continue;
-            const int64_t row = paged_row(s_page[i], H, h, p.shift) + s_slot[i];
-            if (BITS == 4)
-                *reinterpret_cast<uint32_t *>(dst + row * rb + d0 / 2) = w;
-            else if ((lane & 3) < 3)
-                *reinterpret_cast<uint32_t *>(dst + row * rb + (d0 & ~31) * 3 / 8 + (lane & 3) * 4) = w;
-            if (weights != nullptr && blockIdx.z == 0 && d0 == 0) weights[row] = 0.f;
+            const int64_t row = s_row[i];
+            if (!mine || row < 0) continue;
+            *reinterpret_cast<uint32_t *>(word + row) = w;
+            if (zeroes) weights[row / rb + ((int64_t)h << p.shift)] = 0.f;
         }
     }
 }
@@ -130,7 +142,7 @@ __global__ void __launch_bounds__(PG_THREADS)
                             T *__restrict__ out)
 {
     constexpr uint32_t MASK = (1u << BITS) - 1u;
-    __shared__ int s_page[PG_ROWS], s_slot[PG_ROWS];
+    __shared__ int64_t s_row[PG_ROWS];  // byte of head 0's row of each position; -1: none
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t t0 = (int64_t)blockIdx.x * rows_per_cta;
     const int rows = (int)min((int64_t)rows_per_cta, p.T - t0);
@@ -146,45 +158,76 @@ __global__ void __launch_bounds__(PG_THREADS)
                 raise_error(p.err, RPTQ_DEVERR_RANGE);
             }
         }
-        s_page[tid] = page;
-        s_slot[tid] = slot;
+        s_row[tid] = page < 0 ? -1 : (paged_row(page, H, 0, p.shift) + slot) * (D * BITS / 8);
     }
     const int c0 = (blockIdx.y * blockDim.x + tid) * 8;
     const bool live = c0 < H * D;
     const int c = live ? c0 : 0, h = c / D, d0 = c - h * D;
-    float s[8];
-    int z[8];
+    auto cluster_at = [&](int j) {
+        const int k = cluster[c + j];
+        return k >= 0 && k < g ? k : 0;
+    };
+    f32x2 s2[4], nz2[4];
+    bool near = true;  // every zero point small enough for the exact difference below
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        int k = cluster[c + i];
-        if (k < 0 || k >= g) {
-            raise_error(p.err, RPTQ_DEVERR_CLUSTER_ID);
-            k = 0;
+    for (int j = 0; j < 4; ++j) {
+        int z[2];
+        float s[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int k = cluster[c + 2 * j + e];
+            if (k < 0 || k >= g) raise_error(p.err, RPTQ_DEVERR_CLUSTER_ID);
+            s[e] = scale[cluster_at(2 * j + e)];
+            z[e] = zero[cluster_at(2 * j + e)];
+            near = near && z[e] > -(1 << 22) && z[e] < (1 << 22);
         }
-        s[i] = scale[k];
-        z[i] = zero[k];
+        s2[j] = mk2(s[0], s[1]);
+        nz2[j] = mk2(-(8388608.f + (float)z[0]), -(8388608.f + (float)z[1]));
     }
     __syncthreads();
     const int rb = D * BITS / 8;
-    const int off = BITS == 4 ? d0 / 2 : (d0 & ~31) * 3 / 8 + min(lane & 3, 2) * 4;
-    for (int i0 = 0; i0 < rows; i0 += PG_UNROLL) {
-        uint32_t w[PG_UNROLL];
+    const uint8_t *word = pages + ((int64_t)h << p.shift) * rb + (BITS == 4 ? d0 / 2 : (d0 & ~31) * 3 / 8 + min(lane & 3, 2) * 4);
+    const int HD = H * D;
+    T *col = out + t0 * HD + c;
+    constexpr int U = PG_UNROLL;
+    uint32_t x[U];  // the next U rows' words, loaded while the U before them are written
+    auto load = [&](int i0) {
 #pragma unroll
-        for (int u = 0; u < PG_UNROLL; ++u) {
-            const int i = min(i0 + u, rows - 1);
-            const int64_t row = paged_row(max(s_page[i], 0), H, h, p.shift) + s_slot[i];
-            w[u] = ldg_stream32(pages + row * rb + off);
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = s_row[min(i0 + u, rows - 1)];
+            x[u] = ldg_stream32(word + max(row, (int64_t)0));
         }
+    };
+    load(0);
+    for (int i0 = 0; i0 < rows; i0 += U) {
+        uint32_t w[U];
 #pragma unroll
-        for (int u = 0; u < PG_UNROLL; ++u) {
+        for (int u = 0; u < U; ++u) w[u] = x[u];
+        if (i0 + U < rows) load(i0 + U);
+        if (i0 > 0) col += U * (int64_t)HD;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             const int i = i0 + u;
             if (i >= rows) break;
             const uint32_t grp = BITS == 4 ? w[u] : unpack_a3_words(w[u], lane);
-            if (!live || s_page[i] < 0) continue;
+            if (!live || s_row[i] < 0) continue;
             float v[8];
+            if (near) {  // 2^23 + code less 2^23 + z: code - z exactly
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = s[j] * (float)((int)((grp >> (BITS * j)) & MASK) - z[j]);
-            store8(out + (t0 + i) * H * D + c, v);
+                for (int j = 0; j < 4; ++j) {
+                    const f32x2 q = mk2(__uint_as_float((grp >> (2 * BITS * j)) & MASK | 0x4B000000u),
+                                        __uint_as_float((grp >> (2 * BITS * j + BITS)) & MASK | 0x4B000000u));
+                    const f32x2 r = mul2(s2[j], add2(q, nz2[j]));
+                    v[2 * j] = lo2(r), v[2 * j + 1] = hi2(r);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int k = cluster_at(j);
+                    v[j] = scale[k] * (float)((int)((grp >> (BITS * j)) & MASK) - zero[k]);
+                }
+            }
+            store8(col + u * HD, v);
         }
     }
 }
