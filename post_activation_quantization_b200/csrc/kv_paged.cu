@@ -4,11 +4,15 @@
 // cluster) and closing memory paragraph (the cache dominates memory at large batch x sequence): the
 // same codes as the dense cache's, in pages, so that sequences of unequal length share one pool
 // (kv_paged.cuh has the layout).
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "kv_codec.cuh"
 #include "kv_paged.cuh"
 #include "launch.h"
+
+namespace cg = cooperative_groups;
 
 namespace rptq {
 
@@ -18,7 +22,7 @@ namespace rptq {
 // tensor.  Where each row of the chunk lives is looked up once per CTA.  Both directions move each
 // byte once and are bound by HBM at large batches and by the launch at small ones.
 constexpr int PG_THREADS = 256;
-constexpr int PG_ROWS = 64;  // most rows of a CTA's chunk
+constexpr int PG_ROWS = 256;  // most rows of a CTA's chunk
 constexpr int PG_UNROLL = 4;  // 16-byte loads (words, for the read-back) of a step, the next step's issued before it
 
 // Four lanes' 24-bit groups <-> the three 32-bit words they fill (lane j of the four holds word j < 3).
@@ -51,18 +55,18 @@ __global__ void __launch_bounds__(PG_THREADS, 2)
     uint8_t *dst = t.dst[blockIdx.z];
     const int64_t t0 = (int64_t)blockIdx.x * rows_per_cta;
     const int rows = (int)min((int64_t)rows_per_cta, p.T - t0);
-    if (tid < rows) {
+    for (int r = tid; r < rows; r += blockDim.x) {
         int page = -1, slot = 0;
-        const int b = paged_row_sequence(p, t0 + tid);
+        const int b = paged_row_sequence(p, t0 + r);
         int s0, n, L;
         if (b >= 0 && paged_sequence(p, b, s0, n, L)) {
-            const int pos = L - n + (int)(t0 + tid - s0);
+            const int pos = L - n + (int)(t0 + r - s0);
             if (pos >= 0) {
                 page = paged_page(p, b, pos >> p.shift);
                 slot = pos & ((1 << p.shift) - 1);
             }
         }
-        s_row[tid] = page < 0 ? -1 : (paged_row(page, H, 0, p.shift) + slot) * (D * BITS / 8);
+        s_row[r] = page < 0 ? -1 : (paged_row(page, H, 0, p.shift) + slot) * (D * BITS / 8);
     }
     const int c0 = (blockIdx.y * blockDim.x + tid) * 8;
     const bool live = c0 < H * D;
@@ -146,11 +150,11 @@ __global__ void __launch_bounds__(PG_THREADS)
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t t0 = (int64_t)blockIdx.x * rows_per_cta;
     const int rows = (int)min((int64_t)rows_per_cta, p.T - t0);
-    if (tid < rows) {
+    for (int r = tid; r < rows; r += blockDim.x) {
         int page = -1, slot = 0;
-        const int b = paged_row_sequence(p, t0 + tid);
+        const int b = paged_row_sequence(p, t0 + r);
         if (b >= 0) {  // p.lens: the first position read of each sequence
-            const int64_t pos = (int64_t)p.lens[b] + (t0 + tid - p.start[b]);
+            const int64_t pos = (int64_t)p.lens[b] + (t0 + r - p.start[b]);
             if (pos >= 0 && pos < p.max_len) {
                 page = paged_page(p, b, (int)(pos >> p.shift));
                 slot = (int)pos & ((1 << p.shift) - 1);
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(PG_THREADS)
                 raise_error(p.err, RPTQ_DEVERR_RANGE);
             }
         }
-        s_row[tid] = page < 0 ? -1 : (paged_row(page, H, 0, p.shift) + slot) * (D * BITS / 8);
+        s_row[r] = page < 0 ? -1 : (paged_row(page, H, 0, p.shift) + slot) * (D * BITS / 8);
     }
     const int c0 = (blockIdx.y * blockDim.x + tid) * 8;
     const bool live = c0 < H * D;
@@ -232,13 +236,14 @@ __global__ void __launch_bounds__(PG_THREADS)
     }
 }
 
-// Rows of a CTA: as many as leave about two CTAs for every SM, at most PG_ROWS.
-static void paged_rows_grid(int64_t T, int C, int tensors, int num_sms, int *threads, int *rows, dim3 *grid)
+// Rows of a CTA: `per_sm` CTAs to an SM, about two waves, where PG_ROWS rows are enough.  A CTA begins with the look-up of
+// its channels' clusters, so few long ones (at 15300 rows of 12288 channels: 32 rows to a CTA 218 us, one wave 181, two 173).
+static void paged_rows_grid(int64_t T, int C, int tensors, int num_sms, int per_sm, int *threads, int *rows, dim3 *grid)
 {
     *threads = std::min(PG_THREADS, (C / 8 + 31) / 32 * 32);
     const int slabs = (C / 8 + *threads - 1) / *threads;
-    const int64_t want = T * slabs * tensors / (2 * num_sms);
-    *rows = (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min(PG_ROWS, *threads)));
+    const int64_t ctas = std::max(1, per_sm * num_sms / (slabs * tensors));  // in the row direction
+    *rows = (int)std::max<int64_t>(1, std::min<int64_t>((T + ctas - 1) / ctas, PG_ROWS));
     *grid = dim3((unsigned)((T + *rows - 1) / *rows), (unsigned)slabs, (unsigned)tensors);
 }
 
@@ -249,7 +254,7 @@ static cudaError_t launch_paged_append_t(const PagedAppendArgs &a)
     const Paged p{a.start, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, 0x7fffffff, a.max_len, a.err};
     int threads, rows;
     dim3 grid;
-    paged_rows_grid(a.T, a.H * a.D, 2, a.num_sms, &threads, &rows, &grid);
+    paged_rows_grid(a.T, a.H * a.D, 2, a.num_sms, 4, &threads, &rows, &grid);
     if (a.bits == 4)
         kv_paged_append_kernel<T, 4><<<grid, threads, 0, a.stream>>>(t, p, a.row_stride, a.H, a.D, a.g, rows, a.weights);
     else
@@ -272,7 +277,7 @@ static cudaError_t launch_paged_dequant_t(const PagedDequantArgs &a)
     const Paged p{a.start, a.begin, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, 0x7fffffff, a.max_len, a.err};
     int threads, rows;
     dim3 grid;
-    paged_rows_grid(a.T, a.H * a.D, 1, a.num_sms, &threads, &rows, &grid);
+    paged_rows_grid(a.T, a.H * a.D, 1, a.num_sms, 8, &threads, &rows, &grid);
     T *out = static_cast<T *>(a.out);
     if (a.bits == 4)
         kv_paged_dequant_kernel<T, 4><<<grid, threads, 0, a.stream>>>(a.pages, p, a.H, a.D, a.cluster, a.scale, a.zero,
@@ -293,15 +298,20 @@ cudaError_t launch_paged_dequant(const PagedDequantArgs &a)
 }
 
 // ---- eviction --------------------------------------------------------------------------------------
-// One CTA per (sequence, head).  The weights' order is that of an unsigned key; the key of the m-th
-// largest candidate is found by four passes of an 8-bit histogram from the top byte down (a radix
-// select), `ties` of the candidates equal to it are kept, lowest positions first.  Two passes over the
-// positions, every warp over its own contiguous range, then count and write the kept positions in
-// order.  Entry j of that list moves from position kept[j] >= j to j: a batch of rows is loaded by the
-// whole CTA, then stored.  A row stored at j < i is never one that a later entry i reads (kept[i] >= i),
-// so the only hazard is inside a batch, and one barrier between its loads and stores covers it.
+// One cluster of CTAs per (sequence, head): each CTA has a contiguous share of the positions, whose keys (an unsigned
+// number in the weights' order) it reads once into shared memory, many loads in flight.  The key of the m-th largest
+// candidate is found by four passes of an 8-bit histogram from the top byte down (a radix select), each pass summed over
+// the cluster through distributed shared memory; `ties` of the candidates equal to it are kept, lowest positions
+// first.  With the shares' counts exchanged every CTA writes its part of the list of kept positions.  Entry j of that
+// list moves from position kept[j] >= j to j: a batch of rows is loaded by the whole cluster, then stored.  A row
+// stored at j < i is never one that a later entry i reads (kept[i] >= i), so the only hazard is inside a batch, and one
+// cluster barrier between its loads and stores covers it.  The bound is the latency of those steps, so few (sequence, head)
+// pairs get a wide cluster.
 constexpr int EV_THREADS = 1024, EV_WARPS = EV_THREADS / 32;
-constexpr int EV_UNITS = 4;  // units of a batch per thread
+constexpr int EV_UNITS = 4;   // units of a batch per thread
+constexpr int EV_LOADS = 8;   // weights of a thread in flight together
+constexpr int EV_MAX_CLUSTER = 8;
+constexpr int EV_KEYS = 48 * 1024;  // keys that fit a CTA's shared memory; beyond, they are read again in every pass
 
 // Larger weight, larger key; both zeros alike; NaN below everything.
 __device__ __forceinline__ uint32_t weight_key(float w)
@@ -314,51 +324,82 @@ __device__ __forceinline__ uint32_t weight_key(float w)
 template <typename U>
 __global__ void __launch_bounds__(EV_THREADS)
     kv_paged_evict_kernel(uint8_t *__restrict__ kq, uint8_t *__restrict__ vq, float *__restrict__ weights, Paged p, int H,
-                          int rb, int budget, int recent, int32_t *__restrict__ new_lens, int32_t *__restrict__ kept)
+                          int rb, int budget, int recent, int cached, int32_t *__restrict__ new_lens, int32_t *__restrict__ kept)
 {
-    __shared__ int hist[256];
-    __shared__ int s_eq[EV_WARPS], s_keep[EV_WARPS], s_digit, s_need, s_bad;
+    extern __shared__ uint32_t s_key[];  // the share's keys, where `cached` of them fit
+    __shared__ int hist[2][256], total[256];
+    __shared__ int s_eq[EV_WARPS], s_keep[EV_WARPS], s_digit, s_need, s_bad, s_first;
+    __shared__ int s_share[2];  // equal candidates, kept others of this CTA
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x / H, h = blockIdx.x % H;
-    int32_t *list = kept + (int64_t)blockIdx.x * budget;
+    const int bh = blockIdx.x / CS, b = bh / H, h = bh % H;
+    int32_t *list = kept + (int64_t)bh * budget;
     const int L = p.lens[b];
     const int32_t *tab = p.table + (int64_t)b * p.max_pages;
     const int pmask = (1 << p.shift) - 1;
-    if (tid == 0) s_bad = 0;
+    if (tid == 0) s_bad = 0, s_first = 0x7fffffff;
+    if (tid < 256) hist[0][tid] = 0;
     __syncthreads();
     bool bad = L < 0 || L > p.max_len;
     if (bad && tid == 0) raise_error(p.err, RPTQ_DEVERR_RANGE);
-    if (!bad && L > budget)  // an evicted sequence's pages are all checked before anything moves
+    if (!bad && L > budget)  // an evicted sequence's pages are all checked, by every CTA, before anything moves
         for (int i = tid; i < (L + pmask) >> p.shift; i += EV_THREADS)
             if (paged_page(p, b, i) < 0) s_bad = 1;
     __syncthreads();
     bad |= s_bad != 0;
-    if (h == 0 && tid == 0) new_lens[b] = bad ? L : min(L, budget);
-    if (bad || L <= budget) {
+    if (h == 0 && rank == 0 && tid == 0) new_lens[b] = bad ? L : min(L, budget);
+    if (bad || L <= budget) {  // the same in every CTA of the cluster
         const int n = bad ? 0 : L;
-        for (int j = tid; j < budget; j += EV_THREADS) list[j] = j < n ? j : -1;
+        for (int j = rank * EV_THREADS + tid; j < budget; j += CS * EV_THREADS) list[j] = j < n ? j : -1;
         return;
     }
     auto row_of = [&](int pos) -> int64_t { return paged_row(tab[pos >> p.shift], H, h, p.shift) + (pos & pmask); };
-    const int cand = L - recent;  // candidates; budget - recent of them stay
+    const int share = ((L + CS - 1) / CS + 31) & ~31;
+    const int x0 = min(L, rank * share), x1 = min(L, x0 + share);  // this CTA's positions
+    const bool in_smem = share <= cached;
+    if (in_smem)
+        for (int i0 = x0; i0 < x1; i0 += EV_THREADS * EV_LOADS) {
+            float w[EV_LOADS];
+#pragma unroll
+            for (int k = 0; k < EV_LOADS; ++k) {
+                const int pos = i0 + k * EV_THREADS + tid;
+                w[k] = pos < x1 ? weights[row_of(pos)] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < EV_LOADS; ++k) {
+                const int pos = i0 + k * EV_THREADS + tid;
+                if (pos < x1) s_key[pos - x0] = weight_key(w[k]);
+            }
+        }
+    __syncthreads();
+    auto key_of = [&](int pos) { return in_smem ? s_key[pos - x0] : weight_key(weights[row_of(pos)]); };
+    const int cand = L - recent;  // candidates: the positions below; budget - recent of them stay
+    const int c1 = min(x1, cand);
     uint32_t prefix = 0, mask = 0;
     int need = budget - recent;
-    for (int sh = 24; sh >= 0 && need > 0; sh -= 8) {
-        for (int i = tid; i < 256; i += EV_THREADS) hist[i] = 0;
-        __syncthreads();
-        for (int i0 = warp * 32; i0 < cand; i0 += EV_THREADS) {
+    for (int sh = 24, pass = 0; sh >= 0 && need > 0; sh -= 8, ++pass) {
+        int *mine = hist[pass & 1];
+        for (int i0 = x0 + warp * 32; i0 < c1; i0 += EV_THREADS) {
             const int pos = i0 + lane;
-            const uint32_t key = pos < cand ? weight_key(weights[row_of(pos)]) : 0u;
-            const bool in = pos < cand && (key & mask) == prefix;
+            const uint32_t key = pos < c1 ? key_of(pos) : 0u;
+            const bool in = pos < c1 && (key & mask) == prefix;
             const uint32_t digit = in ? (key >> sh) & 255u : 256u;
             const uint32_t same = __match_any_sync(FULL, digit);
-            if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+            if (in && lane == __ffs(same) - 1) atomicAdd(&mine[digit], __popc(same));
+        }
+        cluster.sync();
+        if (tid < 256) {
+            int t = 0;
+            for (int r = 0; r < CS; ++r) t += cluster.map_shared_rank(mine, r)[tid];
+            total[tid] = t;
+            hist[(pass + 1) & 1][tid] = 0;  // read by others in the pass before only
         }
         __syncthreads();
         if (warp == 0) {  // lane l: bins 255 - 8l .. 248 - 8l; the digit where the count from the top reaches need
             int c[8], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
+            for (int i = 0; i < 8; ++i) sum += c[i] = total[255 - 8 * lane - i];
             int before = sum;
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(FULL, before, o);
@@ -384,52 +425,71 @@ __global__ void __launch_bounds__(EV_THREADS)
     }
     const bool some = budget > recent;  // else no candidate stays
     const int ties = need;
-    // warp w: positions [w0, w1)
-    const int per = ((L + EV_WARPS - 1) / EV_WARPS + 31) & ~31;
-    const int w0 = min(L, warp * per), w1 = min(L, w0 + per);
+    // warp w: positions [w0, w1) of the share
+    const int per = ((x1 - x0 + EV_WARPS - 1) / EV_WARPS + 31) & ~31;
+    const int w0 = min(x1, x0 + warp * per), w1 = min(x1, w0 + per);
     int n_eq = 0, n_gt = 0;  // candidates equal to the threshold; those above it and the recent ones
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const int pos = i0 + lane;
-        const uint32_t key = pos < cand && pos < w1 ? weight_key(weights[row_of(pos)]) : 0u;
         const bool c = pos < cand && pos < w1 && some;
+        const uint32_t key = c ? key_of(pos) : 0u;
         n_eq += __popc(__ballot_sync(FULL, c && key == prefix));
         n_gt += __popc(__ballot_sync(FULL, (c && key > prefix) || (pos >= cand && pos < w1)));
     }
-    if (lane == 0) s_eq[warp] = n_eq;
+    if (lane == 0) s_eq[warp] = n_eq, s_keep[warp] = n_gt;
     __syncthreads();
-    int eq = 0;  // equal candidates before this warp's range
-    for (int w = 0; w < warp; ++w) eq += s_eq[w];
-    if (lane == 0) s_keep[warp] = n_gt + max(0, min(n_eq, ties - eq));
-    __syncthreads();
-    int at = 0;
-    for (int w = 0; w < warp; ++w) at += s_keep[w];
+    if (tid == 0) {
+        int e = 0, g = 0;
+        for (int w = 0; w < EV_WARPS; ++w) e += s_eq[w], g += s_keep[w];
+        s_share[0] = e, s_share[1] = g;
+    }
+    cluster.sync();
+    int eq = 0, at = 0;  // equal candidates, kept positions before this warp's range
+    for (int r = 0; r < rank; ++r) {
+        const int *o = cluster.map_shared_rank(s_share, r);
+        at += o[1] + max(0, min(o[0], ties - eq));
+        eq += o[0];
+    }
+    for (int w = 0; w < warp; ++w) {
+        at += s_keep[w] + max(0, min(s_eq[w], ties - eq));
+        eq += s_eq[w];
+    }
+    int first = 0x7fffffff;  // first entry that moves
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const int pos = i0 + lane;
-        const uint32_t key = pos < cand && pos < w1 ? weight_key(weights[row_of(pos)]) : 0u;
         const bool c = pos < cand && pos < w1 && some;
+        const uint32_t key = c ? key_of(pos) : 0u;
         const uint32_t be = __ballot_sync(FULL, c && key == prefix), below = (1u << lane) - 1u;
         const bool keep = (c && key > prefix) || (pos >= cand && pos < w1) ||
                           (c && key == prefix && eq + __popc(be & below) < ties);
         const uint32_t bk = __ballot_sync(FULL, keep);
-        if (keep) list[at + __popc(bk & below)] = pos;
+        const int j = at + __popc(bk & below);
+        if (keep) {
+            list[j] = pos;
+            if (j != pos) first = min(first, j);
+        }
         eq += __popc(be);
         at += __popc(bk);
     }
-    __syncthreads();
-    // move: units of sizeof(U) bytes, `per_row` to a row of K or V
+    first = __reduce_min_sync(FULL, first);
+    if (lane == 0) atomicMin(&s_first, first);
+    __threadfence();  // the list is read by the other CTAs
+    cluster.sync();
+    for (int r = 0; r < CS; ++r) first = min(first, *cluster.map_shared_rank(&s_first, r));
+    // move: units of sizeof(U) bytes, `per_row` to a row of K or V, then the weights
     const int per_row = rb / (int)sizeof(U);
     const int units = 2 * per_row;
-    const int64_t total = (int64_t)budget * units;
-    for (int64_t u0 = 0; u0 < total; u0 += EV_THREADS * EV_UNITS) {
+    const int64_t end = (int64_t)budget * units;
+    for (int64_t u0 = (int64_t)min(first, budget) * units; u0 < end; u0 += (int64_t)CS * EV_THREADS * EV_UNITS) {
         U v[EV_UNITS];
         U *to[EV_UNITS];
 #pragma unroll
         for (int k = 0; k < EV_UNITS; ++k) {
-            const int64_t u = u0 + k * EV_THREADS + tid;
+            const int64_t u = u0 + ((int64_t)k * CS + rank) * EV_THREADS + tid;
             to[k] = nullptr;
-            if (u < total) {
+            if (u < end) {
                 const int j = (int)(u / units), part = (int)(u - (int64_t)j * units);
-                const int pos = list[j];
+                const int pos = __ldcg(list + j);
                 if (pos != j) {
                     uint8_t *base = part < per_row ? kq : vq;
                     const int o = part < per_row ? part : part - per_row;
@@ -438,33 +498,48 @@ __global__ void __launch_bounds__(EV_THREADS)
                 }
             }
         }
-        __syncthreads();
+        cluster.sync();
 #pragma unroll
         for (int k = 0; k < EV_UNITS; ++k)
             if (to[k] != nullptr) *to[k] = v[k];
     }
-    for (int j0 = 0; j0 < budget; j0 += EV_THREADS) {
-        const int j = j0 + tid;
-        const int pos = j < budget ? list[j] : 0;
+    for (int j0 = min(first, budget); j0 < budget; j0 += CS * EV_THREADS) {
+        const int j = j0 + rank * EV_THREADS + tid;
+        const int pos = j < budget ? __ldcg(list + j) : 0;
         const bool moves = j < budget && pos != j;
-        const float w = moves ? weights[row_of(pos)] : 0.f;
-        __syncthreads();
+        const float w = moves ? __ldcg(weights + row_of(pos)) : 0.f;
+        cluster.sync();
         if (moves) weights[row_of(j)] = w;
     }
+    cluster.sync();  // the others may still be reading this CTA's shared memory
 }
 
 cudaError_t launch_paged_evict(const PagedEvictArgs &a)
 {
     const Paged p{nullptr, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, 0, 0, a.max_len, a.err};
     const int rb = a.D * a.bits / 8;
-    const unsigned grid = (unsigned)(a.B * a.H);
-    if (rb % 16 == 0)
-        kv_paged_evict_kernel<uint4><<<grid, EV_THREADS, 0, a.stream>>>(a.kq, a.vq, a.weights, p, a.H, rb, a.budget,
-                                                                        a.recent, a.new_lens, a.kept);
-    else
-        kv_paged_evict_kernel<uint32_t><<<grid, EV_THREADS, 0, a.stream>>>(a.kq, a.vq, a.weights, p, a.H, rb, a.budget,
-                                                                           a.recent, a.new_lens, a.kept);
-    return cudaGetLastError();
+    // a CTA to an SM at least, as long as a share has a thousand positions
+    int cs = 1;
+    while (cs < EV_MAX_CLUSTER && (int64_t)a.B * a.H * cs < a.num_sms && a.max_len / (2 * cs) >= EV_THREADS) cs *= 2;
+    const int cached = std::min(EV_KEYS, (a.max_len / cs + 64) & ~31);
+    const void *kern = rb % 16 == 0 ? (const void *)kv_paged_evict_kernel<uint4> : (const void *)kv_paged_evict_kernel<uint32_t>;
+    const size_t smem = (size_t)cached * 4;
+    cudaError_t e = kernel_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.B * a.H * cs));
+    cfg.blockDim = dim3(EV_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cs;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    void *args[] = {(void *)&a.kq, (void *)&a.vq, (void *)&a.weights, (void *)&p, (void *)&a.H, (void *)&rb, (void *)&a.budget,
+                    (void *)&a.recent, (void *)&cached, (void *)&a.new_lens, (void *)&a.kept};
+    return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
 }  // namespace rptq
