@@ -307,7 +307,7 @@ cudaError_t launch_paged_dequant(const PagedDequantArgs &a)
 // stored at j < i is never one that a later entry i reads (kept[i] >= i), so the only hazard is inside a batch, and one
 // cluster barrier between its loads and stores covers it.  The bound is the latency of those steps, so few (sequence, head)
 // pairs get a wide cluster.
-constexpr int EV_THREADS = 1024, EV_WARPS = EV_THREADS / 32;
+constexpr int EV_SMALL = 256;  // threads of a CTA where there are many
 constexpr int EV_UNITS = 4;   // units of a batch per thread
 constexpr int EV_LOADS = 8;   // weights of a thread in flight together
 constexpr int EV_MAX_CLUSTER = 8;
@@ -321,11 +321,12 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-template <typename U>
+template <typename U, int EV_THREADS>
 __global__ void __launch_bounds__(EV_THREADS)
     kv_paged_evict_kernel(uint8_t *__restrict__ kq, uint8_t *__restrict__ vq, float *__restrict__ weights, Paged p, int H,
                           int rb, int budget, int recent, int cached, int32_t *__restrict__ new_lens, int32_t *__restrict__ kept)
 {
+    constexpr int EV_WARPS = EV_THREADS / 32;
     extern __shared__ uint32_t s_key[];  // the share's keys, where `cached` of them fit
     __shared__ int hist[2][256], total[256];
     __shared__ int s_eq[EV_WARPS], s_keep[EV_WARPS], s_digit, s_need, s_bad, s_first;
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(EV_THREADS)
     const int32_t *tab = p.table + (int64_t)b * p.max_pages;
     const int pmask = (1 << p.shift) - 1;
     if (tid == 0) s_bad = 0, s_first = 0x7fffffff;
-    if (tid < 256) hist[0][tid] = 0;
+    for (int i = tid; i < 256; i += EV_THREADS) hist[0][i] = 0;
     __syncthreads();
     bool bad = L < 0 || L > p.max_len;
     if (bad && tid == 0) raise_error(p.err, RPTQ_DEVERR_RANGE);
@@ -389,11 +390,11 @@ __global__ void __launch_bounds__(EV_THREADS)
             if (in && lane == __ffs(same) - 1) atomicAdd(&mine[digit], __popc(same));
         }
         cluster.sync();
-        if (tid < 256) {
+        for (int i = tid; i < 256; i += EV_THREADS) {
             int t = 0;
-            for (int r = 0; r < CS; ++r) t += cluster.map_shared_rank(mine, r)[tid];
-            total[tid] = t;
-            hist[(pass + 1) & 1][tid] = 0;  // read by others in the pass before only
+            for (int r = 0; r < CS; ++r) t += cluster.map_shared_rank(mine, r)[i];
+            total[i] = t;
+            hist[(pass + 1) & 1][i] = 0;  // read by others in the pass before only
         }
         __syncthreads();
         if (warp == 0) {  // lane l: bins 255 - 8l .. 248 - 8l; the digit where the count from the top reaches need
@@ -518,17 +519,22 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a)
 {
     const Paged p{nullptr, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, 0, 0, a.max_len, a.err};
     const int rb = a.D * a.bits / 8;
-    // a CTA to an SM at least, as long as a share has a thousand positions
+    // A CTA to an SM at least, as long as a share has a thousand positions.  Many pairs get small CTAs, whose phases
+    // interleave on an SM (512 pairs of 2000 positions cut to 1024, with the read-back: 128 threads 152 us, 256 125,
+    // 512 134, 1024 160)
     int cs = 1;
-    while (cs < EV_MAX_CLUSTER && (int64_t)a.B * a.H * cs < a.num_sms && a.max_len / (2 * cs) >= EV_THREADS) cs *= 2;
+    while (cs < EV_MAX_CLUSTER && (int64_t)a.B * a.H * cs < a.num_sms && a.max_len / (2 * cs) >= 1024) cs *= 2;
     const int cached = std::min(EV_KEYS, (a.max_len / cs + 64) & ~31);
-    const void *kern = rb % 16 == 0 ? (const void *)kv_paged_evict_kernel<uint4> : (const void *)kv_paged_evict_kernel<uint32_t>;
+    const bool many = (int64_t)a.B * a.H >= 2 * a.num_sms;
+    const void *k16 = many ? (const void *)kv_paged_evict_kernel<uint4, EV_SMALL> : (const void *)kv_paged_evict_kernel<uint4, 1024>;
+    const void *k4 = many ? (const void *)kv_paged_evict_kernel<uint32_t, EV_SMALL> : (const void *)kv_paged_evict_kernel<uint32_t, 1024>;
+    const void *kern = rb % 16 == 0 ? k16 : k4;
     const size_t smem = (size_t)cached * 4;
     cudaError_t e = kernel_smem(kern, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.B * a.H * cs));
-    cfg.blockDim = dim3(EV_THREADS);
+    cfg.blockDim = dim3(many ? EV_SMALL : 1024);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr{};

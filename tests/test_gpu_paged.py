@@ -272,7 +272,8 @@ def test_shared_pages_may_be_read_by_two_sequences():
 @pytest.mark.parametrize("H,D,bits,page,lens,budget,recent", [
     (3, 128, 3, 64, [2000, 1024, 1025, 5], 1024, 100), (2, 64, 3, 16, [40, 33, 32], 32, 32), (1, 32, 4, 16, [17], 16, 0),
     (2, 96, 3, 32, [500, 1], 1, 1), (4, 128, 4, 128, [5000, 4000], 999, 7), (8, 64, 4, 256, [700], 699, 5),
-    (2, 256, 4, 16, [300, 0, 299], 150, 149), (1, 128, 3, 64, [33000], 4096, 511)])
+    (2, 256, 4, 16, [300, 0, 299], 150, 149), (1, 128, 3, 64, [33000], 4096, 511),
+    (100, 32, 4, 16, [70, 64, 33], 33, 5), (2, 128, 4, 128, [9000, 3], 1000, 0)])
 @pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
 def test_eviction_equals_the_definition(H, D, bits, page, lens, budget, recent, kind):
     c = Case(H, D, bits, page, [0] * len(lens), lens, seed=21, sums=True)
