@@ -213,7 +213,7 @@ size_t paged_decode_workspace(int64_t T, int Hq, int H, int D, int dtype, int B,
                               int num_sms);
 cudaError_t launch_paged_decode(const PagedAttnArgs &a);
 // joins the partial results of d.splits parts of the positions
-cudaError_t launch_paged_combine(const PagedAttnDev &d, int D, int B, bool weights, int max_rows, cudaStream_t stream);
+cudaError_t launch_paged_combine(const PagedAttnDev &d, int D, cudaStream_t stream);
 
 // many rows to a K/V head (kv_paged_chunk.cu)
 size_t paged_chunk_workspace(int64_t T, int Hq, int H, int D, int dtype, int B, int max_len, int weights, int num_sms);

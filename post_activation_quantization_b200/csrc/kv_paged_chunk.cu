@@ -799,7 +799,7 @@ ChunkPlan chunk_plan(int64_t T, int Hq, int H, int D, int dtype, int B, int max_
 }
 
 template <int BITS, int D, int QP, int PP>
-cudaError_t launch_chunk(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles, int B, int max_rows, cudaStream_t stream)
+cudaError_t launch_chunk(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles, int B, cudaStream_t stream)
 {
     constexpr size_t qsmem = (size_t)QP * (D / 64) * CH_SLAB;
     cudaError_t e = kernel_smem((const void *)paged_chunk_queries<BITS, D, QP>, qsmem);
@@ -810,7 +810,7 @@ cudaError_t launch_chunk(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles,
         <<<(unsigned)(pl.slots2 * c.a.H * pl.splits), CH_THREADS, ChunkShape<D, QP>::SMEM, stream>>>(c);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (pl.splits > 1 && (e = launch_paged_combine(c.a, D, B, false, max_rows, stream)) != cudaSuccess) return e;
+    if (pl.splits > 1 && (e = launch_paged_combine(c.a, D, stream)) != cudaSuccess) return e;
     if (c.a.weights != nullptr) {
         if constexpr (QP == 2) {
             if ((e = kernel_smem((const void *)paged_chunk_weights<BITS, D>, WeightShape<D>::SMEM)) != cudaSuccess) return e;
@@ -822,11 +822,11 @@ cudaError_t launch_chunk(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles,
     return cudaGetLastError();
 }
 template <int BITS, int D>
-cudaError_t launch_chunk_prec(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles, int B, int max_rows, cudaStream_t stream)
+cudaError_t launch_chunk_prec(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles, int B, cudaStream_t stream)
 {
-    if (c.a.dtype == RPTQ_F32) return launch_chunk<BITS, D, 2, 2>(c, pl, tiles, B, max_rows, stream);
-    if (pl.qp == 2) return launch_chunk<BITS, D, 2, 1>(c, pl, tiles, B, max_rows, stream);
-    return launch_chunk<BITS, D, 1, 1>(c, pl, tiles, B, max_rows, stream);
+    if (c.a.dtype == RPTQ_F32) return launch_chunk<BITS, D, 2, 2>(c, pl, tiles, B, stream);
+    if (pl.qp == 2) return launch_chunk<BITS, D, 2, 1>(c, pl, tiles, B, stream);
+    return launch_chunk<BITS, D, 1, 1>(c, pl, tiles, B, stream);
 }
 }  // namespace
 
@@ -854,12 +854,11 @@ cudaError_t launch_paged_chunk(const PagedAttnArgs &a)
     c.tiles = tiles;
     c.cx = reinterpret_cast<float *>(ws + pl.cx);
     c.slots = pl.slots;
-    const int max_rows = a.max_q * d.G;
     if (a.bits == 4)
-        return a.D == 128 ? launch_chunk_prec<4, 128>(c, pl, tiles, a.B, max_rows, a.stream)
-                          : launch_chunk_prec<4, 64>(c, pl, tiles, a.B, max_rows, a.stream);
-    return a.D == 128 ? launch_chunk_prec<3, 128>(c, pl, tiles, a.B, max_rows, a.stream)
-                      : launch_chunk_prec<3, 64>(c, pl, tiles, a.B, max_rows, a.stream);
+        return a.D == 128 ? launch_chunk_prec<4, 128>(c, pl, tiles, a.B, a.stream)
+                          : launch_chunk_prec<4, 64>(c, pl, tiles, a.B, a.stream);
+    return a.D == 128 ? launch_chunk_prec<3, 128>(c, pl, tiles, a.B, a.stream)
+                      : launch_chunk_prec<3, 64>(c, pl, tiles, a.B, a.stream);
 }
 
 }  // namespace rptq

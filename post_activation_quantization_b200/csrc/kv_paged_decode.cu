@@ -12,26 +12,23 @@
 // A CTA is four warps; warp w of part s of a (sequence, K/V head) takes the tiles of 32 positions
 // s * 4 + w, + 4 * splits, ...  Each warp streams its tiles' K and V rows (contiguous in a page) with
 // bulk copies into a ring of its own, keeps its own running maximum and sum, and needs no other warp until
-// the end, when the CTA joins its warps.  With one part the CTA writes the output; else a second kernel joins
-// the parts, and adds the positions' weights to the running sums from the scores that the first one kept.
+// the end.  Up to eight parts of a (sequence, K/V head) are a cluster: its CTAs join their warps through distributed shared
+// memory, write the outputs, and add to the running sums, each for the positions whose scores it kept.  More parts (long
+// contexts, few heads) are joined by a second kernel.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "kv_paged_attn.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace rptq {
 
 constexpr int DEC_WARPS = 4, DEC_THREADS = 32 * DEC_WARPS;
 constexpr int DEC_TILE = 32;    // positions of a warp's tile: two blocks of 16
-#ifndef STG
-#define STG 4
-#endif
-#ifndef MINB
-#define MINB 4
-#endif
-#ifndef PERSM
-#define PERSM 3
-#endif
-constexpr int DEC_STAGES = STG;   // tiles of a warp's ring
+constexpr int DEC_STAGES = 3;   // tiles of a warp's ring: two on the way while one is worked (four: fewer CTAs to an SM, slower)
+constexpr int DEC_CTAS_SM = 4;  // CTAs that share an SM: 128 registers a thread, 36 or 48 KB of rings
 // Weights are held as 2^y, y = x - m + DEC_PSHIFT for a reference m that follows the running maximum: y up to
 // DEC_YMAX fits fp16, and its smallest step is 2^-(24 + DEC_PSHIFT) of a weight at the reference.
 constexpr int DEC_PSHIFT = 5;
@@ -154,7 +151,7 @@ struct DecShape {
 };
 
 template <int BITS, int D, int RT, int NT, int PREC>
-__global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
+__global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ? 3 : 2)
     paged_decode_kernel(const PagedAttnDev a)
 {
     using S = DecShape<BITS, D, RT, NT, PREC>;
@@ -167,6 +164,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
     __shared__ float s_sk[D], s_sv[D], s_zv[D];
     __shared__ __align__(16) float s_q[S::ROWS * D];
     __shared__ __align__(16) uint8_t s_ref[S::RB];
+    __shared__ float s_fac[S::ROWS][32], s_max[S::ROWS], s_inv[S::ROWS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
     const Paged &p = a.p;
     const int split = blockIdx.x % a.splits;
@@ -526,24 +524,21 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
             }
         }
     __syncthreads();
-    for (int i = tid; i < rows * D; i += DEC_THREADS) {
-        const int r = i / D, d = i - r * D;
-        const int tok = r / a.G, j = r - tok * a.G;
-        const int64_t row = (int64_t)(s0 + tok) * a.Hq + h * a.G + j;
-        float mt = -INFINITY, lt = 0.f, v = 0.f;
+    auto row_of = [&](int r) { return (int64_t)(s0 + r / a.G) * a.Hq + h * a.G + r % a.G; };
+    if (a.part != nullptr) {  // more parts than a cluster has CTAs: a second kernel joins them
+        for (int i = tid; i < rows * D; i += DEC_THREADS) {
+            const int r = i / D, d = i - r * D;
+            const int64_t row = row_of(r);
+            float mt = -INFINITY, lt = 0.f, v = 0.f;
 #pragma unroll
-        for (int w = 0; w < DEC_WARPS; ++w) mt = fmaxf(mt, jm[w * S::ROWS + r]);
+            for (int w = 0; w < DEC_WARPS; ++w) mt = fmaxf(mt, jm[w * S::ROWS + r]);
 #pragma unroll
-        for (int w = 0; w < DEC_WARPS; ++w) {
-            const float mw = jm[w * S::ROWS + r];
-            const float f = mw == -INFINITY ? 0.f : ex2(mw - mt);
-            lt = fmaf(jl[w * S::ROWS + r], f, lt);
-            v = fmaf(js[(w * S::ROWS + r) * D + d], f, v);
-        }
-        if (a.part == nullptr) {
-            const bool sees = mt != -INFINITY;
-            store_elem(a.out, a.dtype, row * D + d, sees ? s_sv[d] * (v / lt - s_zv[d]) : 0.f);
-        } else {
+            for (int w = 0; w < DEC_WARPS; ++w) {
+                const float mw = jm[w * S::ROWS + r];
+                const float f = mw == -INFINITY ? 0.f : ex2(mw - mt);
+                lt = fmaf(jl[w * S::ROWS + r], f, lt);
+                v = fmaf(js[(w * S::ROWS + r) * D + d], f, v);
+            }
             a.part[((int64_t)split * p.T * a.Hq + row) * D + d] = v;
             if (d == 0) {
                 float *ml = a.ml + ((int64_t)split * p.T * a.Hq + row) * 2;
@@ -551,80 +546,103 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? MINB : NT == 2 ? 3 : 2)
                 ml[1] = lt;
             }
         }
+        return;
     }
+    // the parts are the CTAs of this cluster: every CTA takes the rows' maxima and sums over all their warps, its share of
+    // the outputs, and (running sums) the positions that it scored itself
+    cg::cluster_group cluster = cg::this_cluster();
+    const int all = a.splits * DEC_WARPS;  // warps of the cluster
+    cluster.sync();
+    for (int r = warp; r < rows; r += DEC_WARPS) {
+        const float *om = cluster.map_shared_rank(jm, min(lane / DEC_WARPS, a.splits - 1));
+        const float *ol = om + (jl - jm);
+        const float mw = lane < all ? om[lane % DEC_WARPS * S::ROWS + r] : -INFINITY;
+        float mt = mw;
+        for (int f = 16; f > 0; f >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, f));
+        const float f = mw == -INFINITY ? 0.f : ex2(mw - mt);
+        float lt = lane < all ? ol[lane % DEC_WARPS * S::ROWS + r] * f : 0.f;
+        for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(FULL, lt, o);
+        s_fac[r][lane] = f;
+        if (lane == 0) s_max[r] = mt, s_inv[r] = mt == -INFINITY ? 0.f : 1.f / lt;
+    }
+    __syncthreads();
+    for (int i = split * DEC_THREADS + tid; i < rows * D; i += a.splits * DEC_THREADS) {
+        const int r = i / D, d = i - r * D;
+        float v = 0.f;
+        for (int c = 0; c < a.splits; ++c) {
+            const float *os = cluster.map_shared_rank(js, c);
+#pragma unroll
+            for (int w = 0; w < DEC_WARPS; ++w) v = fmaf(os[(w * S::ROWS + r) * D + d], s_fac[r][c * DEC_WARPS + w], v);
+        }
+        store_elem(a.out, a.dtype, row_of(r) * D + d, s_max[r] == -INFINITY ? 0.f : s_sv[d] * (v * s_inv[r] - s_zv[d]));
+    }
+    if (a.weights != nullptr) {
+        constexpr int U = 8;  // tiles whose loads are in flight together
+        for (int i0 = 0; i0 < count; i0 += U) {
+            int pos[U];
+            float *at[U], old[U], w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                pos[u] = i0 + u < count ? (first + (i0 + u) * stride) * DEC_TILE + lane : L;
+                const int page = pos[u] < L ? paged_page(p, b, pos[u] >> p.shift) : -1;
+                at[u] = page < 0 ? nullptr : a.weights + paged_row(page, a.H, h, p.shift) + (pos[u] & ((1 << p.shift) - 1));
+                w[u] = 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) old[u] = at[u] ? *at[u] : 0.f;
+            for (int r = 0; r < rows; ++r) {
+                const float *x = a.scores + row_of(r) * p.max_len;
+                const int seen = L - n + r / a.G + 1;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (at[u] && pos[u] < seen) w[u] = fmaf(ex2(x[pos[u]] - s_max[r]), s_inv[r], w[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (at[u]) *at[u] = old[u] + w[u];
+        }
+    }
+    cluster.sync();  // the others may still be reading this CTA's shared memory
 }
 
-// Joins the parts of every row (the first T Hq CTAs, one to a row), and adds the weights (the others, one to a
-// block of CMB_KEYS positions of a (sequence, K/V head)).
-constexpr int CMB_THREADS = 128, CMB_KEYS = 512;
-
-// Base-2 maximum and sum of a row over its parts, by one warp: every lane gets them.
-__device__ __forceinline__ void join_parts(const float *ml, int64_t R, int64_t row, int splits, float &mt, float &lt)
-{
-    const int lane = threadIdx.x & 31;
-    mt = -INFINITY;
-    lt = 0.f;
-    for (int s = lane; s < splits; s += 32) mt = fmaxf(mt, ml[(s * R + row) * 2]);
-    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, o));
-    if (mt == -INFINITY) return;
-    for (int s = lane; s < splits; s += 32) lt += ml[(s * R + row) * 2 + 1] * ex2(ml[(s * R + row) * 2] - mt);
-    for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(FULL, lt, o);
-}
+// Joins the parts of every row, a CTA to a row.
+constexpr int CMB_THREADS = 128;
 
 template <int D>
 __global__ void __launch_bounds__(CMB_THREADS)
-    paged_combine_kernel(const PagedAttnDev a, int blocks)
+    paged_combine_kernel(const PagedAttnDev a)
 {
-    extern __shared__ float s_f[];  // a factor per part, or per row the maximum and the sum's reciprocal
+    extern __shared__ float s_f[];  // a factor per part
     const Paged &p = a.p;
-    const int tid = threadIdx.x;
-    const int64_t R = p.T * a.Hq;
-    if (blockIdx.x < R) {
-        const int64_t row = blockIdx.x, t = row / a.Hq;
-        const int b = paged_row_sequence(p, t);
-        int s0, n, L;
-        if (b < 0 || !paged_sequence(p, b, s0, n, L)) return;
-        float mt, lt;
-        join_parts(a.ml, R, row, a.splits, mt, lt);
-        for (int s = tid; s < a.splits; s += CMB_THREADS) {
-            const float ms = a.ml[(s * R + row) * 2];
-            s_f[s] = ms == -INFINITY ? 0.f : ex2(ms - mt) / lt;
-        }
-        __syncthreads();
-        if (a.stat != nullptr && tid == 0) {
-            a.stat[2 * row] = mt == -INFINITY ? 0.f : mt;
-            a.stat[2 * row + 1] = mt == -INFINITY ? 0.f : 1.f / lt;
-        }
-        const int h = (int)(row % a.Hq) / a.G;
-        for (int d = tid; d < D; d += CMB_THREADS) {
-            float v = 0.f;
-#pragma unroll 8
-            for (int s = 0; s < a.splits; ++s) v = fmaf(a.part[(s * R + row) * D + d], s_f[s], v);
-            const int k = cluster_of(a.kt.cv, h * D + d, a.kt.g, p.err);
-            store_elem(a.out, a.dtype, row * D + d, mt == -INFINITY ? 0.f : a.kt.sv[k] * (v - ((float)a.kt.zv[k] - a.mid)));
-        }
-        return;
-    }
-    const int64_t u = blockIdx.x - R;
-    const int blk = (int)(u % blocks), bh = (int)(u / blocks), b = bh / a.H, h = bh % a.H;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t R = p.T * a.Hq, row = blockIdx.x;
+    const int b = paged_row_sequence(p, row / a.Hq);
     int s0, n, L;
-    if (!paged_sequence(p, b, s0, n, L)) return;
-    const int rows = n * a.G;
-    if (rows == 0 || blk * CMB_KEYS >= L) return;
-    auto row_of = [&](int r) { return (int64_t)(s0 + r / a.G) * a.Hq + h * a.G + r % a.G; };
-    for (int r = tid >> 5; r < rows; r += CMB_THREADS / 32) {
-        float mt, lt;
-        join_parts(a.ml, R, row_of(r), a.splits, mt, lt);
-        // (the log of the sum, added to a maximum of some thousands, would lose the sum's low bits)
-        if ((tid & 31) == 0) s_f[2 * r] = mt, s_f[2 * r + 1] = mt == -INFINITY ? 0.f : 1.f / lt;
+    if (b < 0 || !paged_sequence(p, b, s0, n, L)) return;
+    float mt = -INFINITY, lt = 0.f;  // the same in every warp
+    for (int s = lane; s < a.splits; s += 32) mt = fmaxf(mt, a.ml[(s * R + row) * 2]);
+    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, o));
+    for (int s = lane; s < a.splits; s += 32) {
+        const float ms = a.ml[(s * R + row) * 2];
+        if (ms != -INFINITY) lt = fmaf(a.ml[(s * R + row) * 2 + 1], ex2(ms - mt), lt);
+    }
+    for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(FULL, lt, o);
+    for (int s = tid; s < a.splits; s += CMB_THREADS) {
+        const float ms = a.ml[(s * R + row) * 2];
+        s_f[s] = ms == -INFINITY ? 0.f : ex2(ms - mt) / lt;
     }
     __syncthreads();
-    for (int pos = blk * CMB_KEYS + tid; pos < min(L, (blk + 1) * CMB_KEYS); pos += CMB_THREADS) {
-        float w = 0.f;
-        for (int r = 0; r < rows; ++r)
-            if (pos <= L - n + r / a.G) w = fmaf(ex2(a.scores[row_of(r) * p.max_len + pos] - s_f[2 * r]), s_f[2 * r + 1], w);
-        const int page = paged_page(p, b, pos >> p.shift);
-        if (page >= 0) a.weights[paged_row(page, a.H, h, p.shift) + (pos & ((1 << p.shift) - 1))] += w;
+    if (a.stat != nullptr && tid == 0) {
+        a.stat[2 * row] = mt == -INFINITY ? 0.f : mt;
+        a.stat[2 * row + 1] = mt == -INFINITY ? 0.f : 1.f / lt;
+    }
+    const int h = (int)(row % a.Hq) / a.G;
+    for (int d = tid; d < D; d += CMB_THREADS) {
+        float v = 0.f;
+#pragma unroll 8
+        for (int s = 0; s < a.splits; ++s) v = fmaf(a.part[(s * R + row) * D + d], s_f[s], v);
+        const int k = cluster_of(a.kt.cv, h * D + d, a.kt.g, p.err);
+        store_elem(a.out, a.dtype, row * D + d, mt == -INFINITY ? 0.f : a.kt.sv[k] * (v - ((float)a.kt.zv[k] - a.mid)));
     }
 }
 
@@ -632,8 +650,9 @@ __global__ void __launch_bounds__(CMB_THREADS)
 namespace {
 struct DecPlan {
     int prec, rt, nt, splits;
+    bool second;  // a second kernel joins the parts
 };
-constexpr int DEC_MAX_SPLITS = 64;
+constexpr int DEC_MAX_SPLITS = 64, DEC_CLUSTER = 8;
 DecPlan dec_plan(int Hq, int H, int dtype, int B, int max_q, int max_len, int weights, int num_sms)
 {
     DecPlan pl;
@@ -641,10 +660,17 @@ DecPlan dec_plan(int Hq, int H, int dtype, int B, int max_q, int max_len, int we
     pl.prec = dtype == RPTQ_F32 ? 2 : weights || dtype == RPTQ_F16 ? 1 : 0;
     pl.rt = rows == 1 ? 1 : pl.prec ? 4 : 8;
     pl.nt = rows <= pl.rt ? 1 : rows <= 2 * pl.rt ? 2 : 4;
-    // parts: enough for three CTAs to an SM, each warp at least two tiles
-    const int64_t units = (int64_t)B * H;
-    const int64_t want = (PERSM * num_sms + units - 1) / units, tiles = (max_len + DEC_TILE - 1) / DEC_TILE;
-    pl.splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles / (2 * DEC_WARPS), DEC_MAX_SPLITS}));
+    // Parts: about DEC_CTAS_SM CTAs to an SM in all, each warp at least a tile.  Up to DEC_CLUSTER (always, where running sums are kept)
+    // they are a cluster, which joins itself; more leave their results to a second kernel.
+    const int64_t units = (int64_t)B * H, tiles = (max_len + DEC_TILE - 1) / DEC_TILE;
+    const int64_t want = std::min((DEC_CTAS_SM * num_sms + units / 2) / units, tiles / DEC_WARPS);
+    if (want > DEC_CLUSTER && !weights) {
+        pl.splits = (int)std::min<int64_t>(want, DEC_MAX_SPLITS);
+    } else {
+        pl.splits = 1;
+        while (pl.splits < want && pl.splits < DEC_CLUSTER) pl.splits *= 2;
+    }
+    pl.second = pl.splits > DEC_CLUSTER;
     return pl;
 }
 }  // namespace
@@ -662,7 +688,7 @@ size_t paged_decode_workspace(int64_t T, int Hq, int H, int D, int dtype, int B,
 {
     const DecPlan pl = dec_plan(Hq, H, dtype, B, max_q, max_len, weights, num_sms);
     size_t bytes = 0;
-    if (pl.splits > 1 || weights) bytes += (size_t)pl.splits * T * Hq * (D + 2) * 4;
+    if (pl.second) bytes += (size_t)pl.splits * T * Hq * (D + 2) * 4;
     if (weights) bytes += (size_t)T * Hq * max_len * 4;
     return bytes;
 }
@@ -674,8 +700,23 @@ static cudaError_t launch_dec(const PagedAttnDev &d, const DecPlan &pl, int B, c
     auto kern = paged_decode_kernel<BITS, D, RT, NT, PREC>;
     cudaError_t e = kernel_smem((const void *)kern, S::SMEM);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((int64_t)B * d.H * pl.splits), DEC_THREADS, S::SMEM, stream>>>(d);
-    return cudaGetLastError();
+    const unsigned grid = (unsigned)((int64_t)B * d.H * pl.splits);
+    if (pl.second || pl.splits == 1) {
+        kern<<<grid, DEC_THREADS, S::SMEM, stream>>>(d);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(DEC_THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)pl.splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, d);
 }
 template <int BITS, int D, int RT, int PREC>
 static cudaError_t launch_dec_prec(const PagedAttnDev &d, const DecPlan &pl, int B, cudaStream_t stream)
@@ -703,27 +744,25 @@ cudaError_t launch_paged_decode(const PagedAttnArgs &a)
     d.q = a.q, d.out = a.out, d.dtype = a.dtype, d.Hq = a.Hq, d.H = a.H, d.G = a.Hq / a.H, d.q_stride = a.q_stride;
     d.kq = a.kq, d.vq = a.vq, d.kt = a.kt, d.scale = a.scale, d.weights = a.weights, d.splits = pl.splits;
     d.mid = pl.prec == 2 ? (float)(1 << (a.bits - 1)) : 0.f;
-    const bool join = pl.splits > 1 || a.weights;
-    if (join) {
+    if (a.weights) d.scores = static_cast<float *>(a.ws);
+    if (pl.second) {
         d.part = static_cast<float *>(a.ws);
         d.ml = d.part + (int64_t)pl.splits * a.T * a.Hq * a.D;
-        if (a.weights) d.scores = d.ml + (int64_t)pl.splits * a.T * a.Hq * 2;
     }
     cudaError_t e = a.bits == 4 ? (a.D == 128 ? launch_dec_rows<4, 128>(d, pl, a.B, a.stream) : launch_dec_rows<4, 64>(d, pl, a.B, a.stream))
                                 : (a.D == 128 ? launch_dec_rows<3, 128>(d, pl, a.B, a.stream) : launch_dec_rows<3, 64>(d, pl, a.B, a.stream));
-    if (e != cudaSuccess || !join) return e;
-    return launch_paged_combine(d, a.D, a.B, a.weights != nullptr, a.max_q * d.G, a.stream);
+    if (e != cudaSuccess || !pl.second) return e;
+    return launch_paged_combine(d, a.D, a.stream);
 }
 
-cudaError_t launch_paged_combine(const PagedAttnDev &d, int D, int B, bool weights, int max_rows, cudaStream_t stream)
+cudaError_t launch_paged_combine(const PagedAttnDev &d, int D, cudaStream_t stream)
 {
-    const int blocks = weights ? std::max(1, (d.p.max_len + CMB_KEYS - 1) / CMB_KEYS) : 0;
-    const unsigned grid = (unsigned)(d.p.T * d.Hq + (int64_t)B * d.H * blocks);
-    const size_t smem = std::max<size_t>(d.splits, weights ? (size_t)max_rows * 2 : 0) * 4;
+    const unsigned grid = (unsigned)(d.p.T * d.Hq);
+    const size_t smem = (size_t)d.splits * 4;
     if (D == 128)
-        paged_combine_kernel<128><<<grid, CMB_THREADS, smem, stream>>>(d, blocks);
+        paged_combine_kernel<128><<<grid, CMB_THREADS, smem, stream>>>(d);
     else
-        paged_combine_kernel<64><<<grid, CMB_THREADS, smem, stream>>>(d, blocks);
+        paged_combine_kernel<64><<<grid, CMB_THREADS, smem, stream>>>(d);
     return cudaGetLastError();
 }
 
