@@ -161,14 +161,32 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
     constexpr int XOR = RT == 1 ? 1 : 2;  // lane distance of a row's two parts
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[DEC_WARPS * DEC_STAGES];
-    __shared__ float s_sk[D], s_sv[D], s_zv[D];
-    __shared__ __align__(16) float s_q[S::ROWS * D];
+    constexpr int QP = D + 16;  // q' of a row: its quarters 4 floats further apart (their lanes read at once)
+    __shared__ float s_sv[D], s_zv[D];
+    // q' and the query fragments (as each lane of a warp holds them).  With one column tile, where four CTAs share an SM,
+    // they lie in the last stages of the warps' rings, which no copy uses before the first turn.
+    constexpr bool IN_RING = NT == 1;
+    constexpr int FR = KP::N / DEC_WARPS;  // fragments that a warp makes
+    static_assert(!IN_RING || FR * 128 + (S::ROWS + DEC_WARPS - 1) / DEC_WARPS * QP * 4 <= S::STAGE, "spare stage");
+    __shared__ __align__(16) float s_q[IN_RING ? 4 : S::ROWS * QP];
+    __shared__ uint32_t s_qf[IN_RING ? 1 : NT * KP::N * 32];
+    auto spare = [&](int w) { return smem + (w * DEC_STAGES + DEC_STAGES - 1) * S::STAGE; };
+    auto q_row = [&](int r) {
+        return IN_RING ? reinterpret_cast<float *>(spare(r % DEC_WARPS) + FR * 128) + r / DEC_WARPS * QP : s_q + r * QP;
+    };
+    auto fragment = [&](int nt, int i) {
+        return IN_RING ? reinterpret_cast<uint32_t *>(spare(i / FR)) + i % FR * 32 : s_qf + (nt * KP::N + i) * 32;
+    };
     __shared__ __align__(16) uint8_t s_ref[S::RB];
     __shared__ float s_fac[S::ROWS][32], s_max[S::ROWS], s_inv[S::ROWS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
     const Paged &p = a.p;
     const int split = blockIdx.x % a.splits;
     const int bh = blockIdx.x / a.splits, b = bh / a.H, h = bh % a.H;
+    // what does not hang on the sequence is asked for first: a CTA's start is a chain of loads
+    const bool channel = tid < D;  // the thread's channel is tid
+    const int ck = channel ? cluster_of(a.kt.ck, h * D + tid, a.kt.g, p.err) : 0;
+    const int cv = channel ? cluster_of(a.kt.cv, h * D + tid, a.kt.g, p.err) : 0;
     int s0, n, L;
     if (!paged_sequence(p, b, s0, n, L)) return;
     const int rows = n * a.G;  // (token, head of the group), at most S::ROWS (the launcher's choice from max_q)
@@ -214,27 +232,31 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
     int issued = 0;
     for (; issued < DEC_STAGES - 1 && issued < count; ++issued) issue(issued);
 
-    // ---- the head's channels, then the query fragments ----
-    for (int d = tid; d < D; d += DEC_THREADS) {
-        s_sk[d] = a.kt.sk[cluster_of(a.kt.ck, h * D + d, a.kt.g, p.err)];
-        const int kv = cluster_of(a.kt.cv, h * D + d, a.kt.g, p.err);
-        s_sv[d] = a.kt.sv[kv];
-        s_zv[d] = (float)a.kt.zv[kv] - (PREC == 2 ? VC::MID : 0);
+    // ---- q' = q s of the rows in fp32, position 0's codes, then the query fragments ----
+    if (channel) {
+        const float sk = a.kt.sk[ck];
+        float q[S::ROWS];
+#pragma unroll
+        for (int r = 0; r < S::ROWS; ++r) {
+            const int tok = r / a.G, j = r - tok * a.G;
+            q[r] = r < rows ? load_elem(a.q, a.dtype, (int64_t)(s0 + tok) * a.q_stride + (int64_t)(h * a.G + j) * D + tid) : 0.f;
+        }
+        s_sv[tid] = a.kt.sv[cv];
+        s_zv[tid] = (float)a.kt.zv[cv] - (PREC == 2 ? VC::MID : 0);
+#pragma unroll
+        for (int r = 0; r < S::ROWS; ++r) q_row(r)[tid + tid / (D / 4) * 4] = q[r] * sk;
     }
+    if (L > 0 && tid < S::RB / 4)
+        reinterpret_cast<uint32_t *>(s_ref)[tid] =
+            __ldg(reinterpret_cast<const uint32_t *>(a.kq + paged_row(max(paged_page(p, b, 0), 0), a.H, h, p.shift) * S::RB) + tid);
     __syncthreads();
-    // q' = q s of the rows, in fp32
-    for (int i = tid; i < S::ROWS * D; i += DEC_THREADS) {
-        const int r = i / D, d = i - r * D, tok = r / a.G, j = r - tok * a.G;
-        s_q[i] = r < rows ? load_elem(a.q, a.dtype, (int64_t)(s0 + tok) * a.q_stride + (int64_t)(h * a.G + j) * D + d) * s_sk[d] : 0.f;
-    }
-    __syncthreads();
-    // column gq of tile nt: the lane needs the channels of its quarter in the order of the K pairs
-    uint32_t qf[NT][KP::N];
+    // Column gq of tile nt: the lane needs the channels of its quarter in the order of the K pairs.  All warps hold the same
+    // fragments; each makes a share of them.
     float cx[NT][E];  // base-2 scores of the lane's columns = cx * S
     int vis[NT][E];   // their visible positions (none in a column that holds no row)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const float *v = s_q + (nt * RT + S::row(gq)) * D + tq * (D / 4);
+        const float *v = q_row(nt * RT + S::row(gq)) + tq * (D / 4 + 4);
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 4; i += 4) {
@@ -247,9 +269,10 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
         if (m > 0.f && m < INFINITY) frexpf(m, &ex);  // m < 2^ex
         ex = max(ex, -100);
         const int grid = PREC ? 11 : 15;  // largest |q'| in [2^(grid - 1), 2^grid)
-        const float up = S::used(gq) ? ldexpf(1.f, grid - ex) : 0.f;
+        const float up = S::used(gq) ? __uint_as_float((uint32_t)(127 + grid - ex) << 23) : 0.f;  // 2^(grid - ex)
 #pragma unroll
         for (int i = 0; i < KP::N; ++i) {
+            if (i / FR != warp) continue;
             float w[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -266,7 +289,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
                 }
                 w[e] = f * (1.f / (float)(1 << KP::pos(i, e)));
             }
-            qf[nt][i] = half2_bits(w[0], w[1]);
+            fragment(nt, i)[lane] = half2_bits(w[0], w[1]);
         }
         const float c = ldexpf(a.scale * LOG2E, ex - grid + (PREC ? 10 : 24));
 #pragma unroll
@@ -276,16 +299,18 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
             vis[nt][e] = S::used(col) && r < rows ? L - n + r / a.G + 1 : 0;
         }
     }
+    __syncthreads();
+    uint32_t qf[NT][KP::N];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < KP::N; ++i) qf[nt][i] = fragment(nt, i)[lane];
+    if (IN_RING) __syncthreads();  // read by all: the stages may be filled
 
     // Scores are taken relative to position 0's, subtracted in the (exact) sums of each part: what is left has the size
     // of the scores' spread, while q' code alone carries the channels' means times q.
     float xr[NT][4];  // [2] and [3] equal [0] and [1]
     {
-        if (L > 0)
-            for (int i = tid; i < S::RB / 4; i += DEC_THREADS)
-                reinterpret_cast<uint32_t *>(s_ref)[i] =
-                    __ldg(reinterpret_cast<const uint32_t *>(a.kq + paged_row(max(paged_page(p, b, 0), 0), a.H, h, p.shift) * S::RB) + i);
-        __syncthreads();
         uint32_t kr[KP::N];
         KP::load(s_ref, tq, kr);
         if (PREC) {
