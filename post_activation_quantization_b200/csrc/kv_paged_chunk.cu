@@ -15,8 +15,8 @@
 // Where the scores must be good to fp32 (fp32 queries, or running sums of weights), q' has two fp16 parts on one
 // grid and S takes two products; fp32 outputs have W in two parts as well.
 //
-// Running sums: a third kernel goes over the positions again with the rows' maxima and sums known: a tile of 128
-// positions is the row operand, S^T = K q'^T, so that a thread owns a position and adds its weights in registers,
+// Running sums: a third kernel goes over the positions again with the rows' maxima and sums known: tiles of 128
+// positions are the row operand, S^T = K q'^T, so that a thread owns a position and adds its weights in registers,
 // row tile by row tile, in a fixed order.
 #include <algorithm>
 
@@ -615,13 +615,15 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
 }
 
 // ---- running sums -------------------------------------------------------------------------------------------
-// One CTA per (sequence, head, tile of 128 positions).  Warps 0-3 and 4-7 take the row tiles in turn, a thread to a position;
-// warp 8 issues the MMAs, warp 9 the copies of the query tiles (two in flight).
-constexpr int CW_THREADS = 320;
+// One CTA per (sequence, head, 256 positions), all 512 tensor-memory columns: S^T of two tiles of 128 positions, twice.
+// Warps 0-3 and 4-7 take the row tiles in turn; a thread has one position of each tile, so that what it reads of a row
+// from shared memory (8 bytes for every lane: two clocks of the 128 bytes a clock) serves two weights.  Warp 8 issues the
+// MMAs, warp 9 the copies of the query tiles (two in flight).
+constexpr int CW_THREADS = 320, CW_TILES = 2;
 template <int D>
 struct WeightShape {
     static constexpr uint32_t QT = 2 * (D / 64) * CH_SLAB, KT = (D / 64) * CH_SLAB;
-    static constexpr uint32_t SMEM = 1024 + 2 * QT + KT;
+    static constexpr uint32_t SMEM = 1024 + 2 * QT + CW_TILES * KT;
 };
 template <int BITS, int D>
 __global__ void __launch_bounds__(CW_THREADS, 1)
@@ -632,18 +634,20 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[9];
     __shared__ uint32_t tmem_slot;
-    __shared__ float4 s_row[2][2][CH_M];  // [group][turn][row]: cx, maximum, 1 / sum, visible positions
-    __shared__ float s_sum[CH_M];
+    __shared__ __align__(16) float2 s_row[2][2][CH_M];  // [group][turn][row]: cx, -(maximum + log2 of the sum)
+    __shared__ int s_vis[2][2][CH_M];                   // visible positions
+    __shared__ float2 s_sum[CH_M];
     const PagedAttnDev &a = c.a;
     const Paged &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int blk = blockIdx.x % blocks, bh = blockIdx.x / blocks, b = bh / a.H, h = bh % a.H;
     int s0, n, L;
     if (!paged_sequence(p, b, s0, n, L)) return;
-    const int R = n * a.G, pos0 = blk * CH_KEYS;
-    if (R == 0 || pos0 >= L) return;
+    const int R = n * a.G, first = blk * CW_TILES * CH_KEYS;
+    if (R == 0 || first >= L) return;
+    const int nact = first + CH_KEYS < L ? 2 : 1;  // tiles of positions
     const int64_t qslot = (int64_t)h * c.slots + chunk_base(p, b, a.G, CH_M);
-    const int i0 = (int)((int64_t)max(0, pos0 - (L - n)) * a.G / CH_M), i1 = (R + CH_M - 1) / CH_M;  // row tiles that see the block
+    const int i0 = (int)((int64_t)max(0, first - (L - n)) * a.G / CH_M), i1 = (R + CH_M - 1) / CH_M;  // row tiles that see the block
 
     const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u, sK = sQ + 2 * S::QT;
     const uint32_t bar = smem_u32(bars);
@@ -658,18 +662,19 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         mbar_init(drain, 1);
         fence_mbar_init();
     }
-    if (warp == 8) tc_alloc(smem_u32(&tmem_slot), 256);
-    if (warp < 4) {
-        int r0, t;
-        chunk_share<D>(tid, r0, t);
+    if (warp == 8) tc_alloc(smem_u32(&tmem_slot), 512);
+    const int g = warp >> 2;
+    if (g < nact) {  // warps 0-3 and 4-7 expand a tile of positions each
+        const int pos0 = first + g * CH_KEYS;
+        int r0, t, ids[4];
+        chunk_share<D>(tid & (CH_M - 1), r0, t);
         uint32_t ref[KP::N];
         chunk_reference<BITS, D>(a, b, h, t, ref);
         ChunkCodes<BITS, D> kc;
-        int ids[4];
         chunk_pages(p, b, pos0, L, r0, ids);
         chunk_check(p, ids);
         kc.read(a.kq, p, ids, a.H, h, pos0, L, r0, t);
-        kc.write(sK, r0, t, [&](uint32_t(&x)[KP::N]) {
+        kc.write(sK + g * S::KT, r0, t, [&](uint32_t(&x)[KP::N]) {
 #pragma unroll
             for (int k = 0; k < KP::N; ++k) x[k] = code_up_plus(x[k], ref[k]);
         });
@@ -681,66 +686,93 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     const uint32_t tmem = tmem_slot;
 
     if (warp < 8) {
-        const int g = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
-        const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)g * CH_M;
-        const int pos = pos0 + r;
+        const int quad = warp & 3, r = 32 * quad + lane;
+        const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)g * CW_TILES * CH_M;
+        const int pos = first + r;  // and pos + 128
+        // the thread's row of tile i
+        auto info = [&](int i, float2 &f, int &vis) {
+            const int row = i * CH_M + r;
+            f = make_float2(0.f, -INFINITY);
+            vis = 0;
+            if (i >= i1 || row >= R) return;
+            const int tok = row / a.G, j = row - tok * a.G;
+            const float2 st = *reinterpret_cast<const float2 *>(a.stat + 2 * ((int64_t)(s0 + tok) * a.Hq + h * a.G + j));
+            // scores are relative to position 0's, so the maximum is small enough for the sum's log to be added to it
+            f = make_float2(c.cx[(qslot + i) * CH_M + r], st.y > 0.f ? log2f(st.y) - st.x : st.y == 0.f ? -INFINITY : st.y);
+            vis = L - n + tok + 1;
+        };
         float w0 = 0.f, w1 = 0.f;
         bool ok = true;
+        float2 f;
+        int vis;
+        info(i0 + g, f, vis);
         for (int i = i0 + g, k = 0; i < i1; i += 2, ++k) {  // every warp takes every turn: the barrier counts them
-            const int row = i * CH_M + r;
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (row < R) {
-                const int tok = row / a.G, j = row - tok * a.G;
-                const int64_t orow = (int64_t)(s0 + tok) * a.Hq + h * a.G + j;
-                f = make_float4(c.cx[(qslot + i) * CH_M + r], a.stat[2 * orow], a.stat[2 * orow + 1],
-                                __int_as_float(L - n + tok + 1));
-            }
             s_row[g][k & 1][r] = f;
+            s_vis[g][k & 1][r] = vis;
             asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+            info(i + 2, f, vis);  // in flight during this turn
             ok = ok && __all_sync(FULL, mbar_wait_bounded(s_full + 8 * g, k & 1, p.err));
             if (!ok) continue;
             tc_fence_after();
-            const bool whole = pos0 + CH_KEYS <= L - n + i * CH_M / a.G + 1;  // every row of the tile sees every position
+            const bool whole = first + CW_TILES * CH_KEYS <= L - n + i * CH_M / a.G + 1;  // every row sees every position
+            const float2 *rows = s_row[g][k & 1];
+            const int *seen = s_vis[g][k & 1];
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
-                uint32_t v[32];
-                tc_ld32(tS + 32 * q4, v);
+                uint32_t u[32], v[32];
+                tc_ld32_async(tS + 32 * q4, u);
+                if (nact == 2) tc_ld32_async(tS + CH_M + 32 * q4, v);
+                tc_wait_ld();
+                tc_loaded(u);
+                tc_loaded(v);
+                if (nact == 1) {
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) v[q] = u[q];
+                }
 #pragma unroll
                 for (int q = 0; q < 32; ++q) {
-                    const float4 s = s_row[g][k & 1][32 * q4 + q];
-                    float e = ex2(fmaf(__uint_as_float(v[q]), s.x, -s.y));
-                    if (!whole && pos >= __float_as_int(s.w)) e = 0.f;
-                    if (q & 1)
-                        w1 = fmaf(e, s.z, w1);
-                    else
-                        w0 = fmaf(e, s.z, w0);
+                    const float2 s = rows[32 * q4 + q];
+                    float e0 = ex2(fmaf(__uint_as_float(u[q]), s.x, s.y)), e1 = ex2(fmaf(__uint_as_float(v[q]), s.x, s.y));
+                    if (!whole) {
+                        const int vq = seen[32 * q4 + q];
+                        e0 = pos < vq ? e0 : 0.f;
+                        e1 = pos + CH_KEYS < vq ? e1 : 0.f;
+                    }
+                    w0 += e0;
+                    w1 += e1;
                 }
             }
             tc_fence_before();
             lin_arrive(s_free + 8 * g);
         }
-        const float w = w0 + w1;
-        if (g == 1) s_sum[r] = w;
+        if (g == 1) s_sum[r] = make_float2(w0, w1);
         asm volatile("bar.sync 3, 256;" ::: "memory");
-        if (g == 0 && pos < L) {
-            const int page = paged_page(p, b, pos >> p.shift);
-            if (page >= 0) a.weights[paged_row(page, a.H, h, p.shift) + (pos & ((1 << p.shift) - 1))] += w + s_sum[r];
+        if (g == 0) {
+            const float2 o = s_sum[r];
+            for (int t = 0; t < nact; ++t) {
+                const int at = pos + t * CH_KEYS;
+                if (at >= L) break;
+                const int page = paged_page(p, b, at >> p.shift);
+                if (page >= 0)
+                    a.weights[paged_row(page, a.H, h, p.shift) + (at & ((1 << p.shift) - 1))] += t ? w1 + o.y : w0 + o.x;
+            }
         }
     } else if (warp == 8) {
         if (lane == 0) {
             constexpr uint32_t id = f16_idesc(CH_M, CH_M);
             for (int i = i0, k = 0; i < i1; ++i, ++k) {
-                const int st = k & 1;
+                const int st = k & 1;  // of the query tiles, and the group whose turn it is
                 if (!mbar_wait_bounded(q_full + 8 * st, (k >> 1) & 1, p.err)) break;
                 if (!mbar_wait_bounded(s_free + 8 * st, ((k >> 1) & 1) ^ 1, p.err)) break;
                 tc_fence_after();
+                for (int t = 0; t < nact; ++t)
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        tc_mma_f16_ss(tmem + st * CH_M, sw128_desc(sK + kk / 4 * CH_SLAB) + 2 * (kk % 4),
-                                      sw128_desc(sQ + st * S::QT + (part * (D / 64) + kk / 4) * CH_SLAB) + 2 * (kk % 4), id,
-                                      (part | kk) != 0);
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc_mma_f16_ss(tmem + (2 * st + t) * CH_M, sw128_desc(sK + t * S::KT + kk / 4 * CH_SLAB) + 2 * (kk % 4),
+                                          sw128_desc(sQ + st * S::QT + (part * (D / 64) + kk / 4) * CH_SLAB) + 2 * (kk % 4), id,
+                                          (part | kk) != 0);
                 tc_commit(q_empty + 8 * st);
                 tc_commit(s_full + 8 * st);
             }
@@ -748,7 +780,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             mbar_wait_bounded(drain, 0, p.err);
         }
         __syncwarp();
-    } else {
+    } else if (warp == 9) {
         if (lane == 0) {
             int issued = 0;
             for (int i = i0, k = 0; i < i1; ++i, ++k) {
@@ -768,7 +800,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     __syncthreads();
     if (warp == 8) {
         tc_fence_after();
-        tc_dealloc(tmem, 256);
+        tc_dealloc(tmem, 512);
     }
 }
 
@@ -814,7 +846,7 @@ cudaError_t launch_chunk(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles,
     if (c.a.weights != nullptr) {
         if constexpr (QP == 2) {
             if ((e = kernel_smem((const void *)paged_chunk_weights<BITS, D>, WeightShape<D>::SMEM)) != cudaSuccess) return e;
-            const int blocks = (c.a.p.max_len + CH_KEYS - 1) / CH_KEYS;
+            const int blocks = (c.a.p.max_len + CW_TILES * CH_KEYS - 1) / (CW_TILES * CH_KEYS);
             paged_chunk_weights<BITS, D>
                 <<<(unsigned)((int64_t)B * c.a.H * blocks), CW_THREADS, WeightShape<D>::SMEM, stream>>>(c, blocks);
         }
