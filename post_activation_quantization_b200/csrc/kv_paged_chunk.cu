@@ -19,6 +19,7 @@
 // positions are the row operand, S^T = K q'^T, so that a thread owns a position and adds its weights in registers,
 // row tile by row tile, in a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_paged_attn.cuh"
 #include "tc.cuh"
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             f = make_float2(c.cx[(qslot + i) * CH_M + r], st.y > 0.f ? log2f(st.y) - st.x : st.y == 0.f ? -INFINITY : st.y);
             vis = L - n + tok + 1;
         };
-        float w0 = 0.f, w1 = 0.f;
+        f32x2 w = mk2(0.f, 0.f);  // of pos, pos + 128
         bool ok = true;
         float2 f;
         int vis;
@@ -717,35 +718,36 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             const bool whole = first + CW_TILES * CH_KEYS <= L - n + i * CH_M / a.G + 1;  // every row sees every position
             const float2 *rows = s_row[g][k & 1];
             const int *seen = s_vis[g][k & 1];
+            auto add = [&](auto all) {
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-                uint32_t u[32], v[32];
-                tc_ld32_async(tS + 32 * q4, u);
-                if (nact == 2) tc_ld32_async(tS + CH_M + 32 * q4, v);
-                tc_wait_ld();
-                tc_loaded(u);
-                tc_loaded(v);
-                if (nact == 1) {
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    uint32_t u[32], v[32];
+                    tc_ld32_async(tS + 32 * q4, u);
+                    tc_ld32_async(tS + CH_M + 32 * q4, v);  // (of no use, and not used, without a second tile)
+                    tc_wait_ld();
+                    tc_loaded(u);
+                    tc_loaded(v);
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) v[q] = u[q];
-                }
-#pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                    const float2 s = rows[32 * q4 + q];
-                    float e0 = ex2(fmaf(__uint_as_float(u[q]), s.x, s.y)), e1 = ex2(fmaf(__uint_as_float(v[q]), s.x, s.y));
-                    if (!whole) {
-                        const int vq = seen[32 * q4 + q];
-                        e0 = pos < vq ? e0 : 0.f;
-                        e1 = pos + CH_KEYS < vq ? e1 : 0.f;
+                    for (int q = 0; q < 32; ++q) {
+                        const float2 s = rows[32 * q4 + q];
+                        const f32x2 y = fma2(mk2(__uint_as_float(u[q]), __uint_as_float(v[q])), mk2(s.x, s.x), mk2(s.y, s.y));
+                        f32x2 e = mk2(ex2(lo2(y)), ex2(hi2(y)));
+                        if (!decltype(all)::value) {
+                            const int vq = seen[32 * q4 + q];
+                            e = mk2(pos < vq ? lo2(e) : 0.f, pos + CH_KEYS < vq ? hi2(e) : 0.f);
+                        }
+                        w = add2(w, e);
                     }
-                    w0 += e0;
-                    w1 += e1;
                 }
-            }
+            };
+            if (whole)
+                add(std::true_type());
+            else
+                add(std::false_type());
             tc_fence_before();
             lin_arrive(s_free + 8 * g);
         }
-        if (g == 1) s_sum[r] = make_float2(w0, w1);
+        if (g == 1) s_sum[r] = w;
         asm volatile("bar.sync 3, 256;" ::: "memory");
         if (g == 0) {
             const float2 o = s_sum[r];
@@ -754,7 +756,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
                 if (at >= L) break;
                 const int page = paged_page(p, b, at >> p.shift);
                 if (page >= 0)
-                    a.weights[paged_row(page, a.H, h, p.shift) + (at & ((1 << p.shift) - 1))] += t ? w1 + o.y : w0 + o.x;
+                    a.weights[paged_row(page, a.H, h, p.shift) + (at & ((1 << p.shift) - 1))] += t ? hi2(w) + o.y : lo2(w) + o.x;
             }
         }
     } else if (warp == 8) {
