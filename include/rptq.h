@@ -403,13 +403,17 @@ int rptq_kv_paged_dequant(const uint8_t *pages, int H, int D, int bits, const in
  * A row that sees no position (lens[b] - n + i < 0) gets out = 0.
  *   q, out       [T, Hq, D] of `dtype`; q's rows q_stride elements apart, out's dense.
  *   max_q, max_len  bounds on the new rows and the length of any sequence (host values: they size
- *                the launch; a sequence beyond them is out of range).
+ *                the launch and the workspace; a sequence beyond them is out of range).
  *   scale        > 0, or 0 for 1 / sqrt(D).
  *   weights      NULL, or the running sums to add to.
  *   workspace    rptq_kv_paged_attention_workspace_size(...) bytes (0: may be NULL), 16-byte
  *                aligned; no initialisation, garbage afterwards.  Calls that may overlap need one each.
- * Sums, softmax statistics and outputs before their rounding to `dtype` are fp32.  Results do not
- * change from run to run.  A page id out of range is read as page 0 (no weight is added there).
+ * Sums, softmax statistics and outputs before their rounding to `dtype` are fp32.  For fp16 and
+ * bf16 outputs the operands of the products carry 11 bits (a weight and, for bf16 or many rows, a
+ * query times its scale, rounded to fp16: at most 2^-11 each); for fp32 outputs, and for the scores
+ * behind running sums, 22 or more.  Results do not change from run to run.  A page id out of range is
+ * read as page 0 (no weight is added there).
+ * Fastest for D = 64 and 128, the head sizes of the tensor-core kernels; other D take a general one.
  */
 size_t rptq_kv_paged_attention_workspace_size(int64_t T, int Hq, int H, int D, int dtype, int B,
                                               int max_q, int max_len, int weights);

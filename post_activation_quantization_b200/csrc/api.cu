@@ -533,7 +533,9 @@ int rptq_kv_paged_attention(const void *q, int dtype, int64_t T, int Hq, int H, 
         max_len > ((int64_t)max_pages << shift) || !(scale >= 0.0f) || !(scale < INFINITY))
         return RPTQ_ERR_INVALID_ARG;
     if (q_stride < (int64_t)Hq * D || q_stride * esize(dtype) % 16 != 0) return RPTQ_ERR_INVALID_ARG;
-    if (T * Hq > 0x7fffffffLL || (int64_t)B * H * ((max_len + 3) / 4) + T * Hq > 0x7fffffffLL) return RPTQ_ERR_UNSUPPORTED;
+    if (T > 0x7fffffffLL || T * Hq > 0x7fffffffLL) return RPTQ_ERR_UNSUPPORTED;
+    // a grid of the positions, for the running sums: blocks of 256, or of 4 by the general kernel
+    if (weights && (int64_t)B * H * (max_len / (D == 64 || D == 128 ? 256 : 4) + 1) > 0x7fffffffLL) return RPTQ_ERR_UNSUPPORTED;
     if (T == 0 || B == 0 || max_q == 0) return RPTQ_OK;
     if (!q || !start || !lens || !page_table || !k_pages || !v_pages || !out || !cluster_k || !scale_k || !zero_k ||
         !cluster_v || !scale_v || !zero_v)

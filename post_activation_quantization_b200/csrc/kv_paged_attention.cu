@@ -56,7 +56,7 @@ template <typename T, int BITS>
 __global__ void __launch_bounds__(GA_THREADS)
     paged_attention_general(const T *__restrict__ q, int64_t q_stride, Paged p, int Hq, int H, int D,
                             const uint8_t *__restrict__ kq, const uint8_t *__restrict__ vq, KvTables kt, float scale,
-                            T *__restrict__ out, float *__restrict__ lse)
+                            T *__restrict__ out, float *__restrict__ stat)
 {
     __shared__ float s_m[GA_WARPS], s_l[GA_WARPS], s_o[GA_WARPS][GA_CPL * 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -113,8 +113,12 @@ __global__ void __launch_bounds__(GA_THREADS)
         for (int w = 0; w < GA_WARPS; ++w) v += f[w] == 0.f ? 0.f : s_o[w][d] * f[w];
         out[(t * Hq + a) * D + d] = from_f32<T>(vis > 0 ? v / lt : 0.f);
     }
-    // log2 of the row's sum of 2^x; +inf for a row that sees nothing, so that its weights are 0
-    if (lse != nullptr && threadIdx.x == 0) lse[t * Hq + a] = vis > 0 ? mt + log2f(lt) : INFINITY;
+    // the row's maximum and the reciprocal of its sum, 0 for a row that sees nothing.  (Their one logarithm would be rounded
+    // at the size of the maximum, some thousands where the keys' means are large, and lose the sum's low bits.)
+    if (stat != nullptr && threadIdx.x == 0) {
+        stat[2 * (t * Hq + a)] = vis > 0 ? mt : 0.f;
+        stat[2 * (t * Hq + a) + 1] = vis > 0 ? 1.f / lt : 0.f;
+    }
 }
 
 // One warp per position of a (sequence, K/V head): its weight summed over the rows that see it, in
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(GA_THREADS)
 template <typename T, int BITS>
 __global__ void __launch_bounds__(GA_THREADS)
     paged_weights_general(const T *__restrict__ q, int64_t q_stride, Paged p, int Hq, int H, int D,
-                          const uint8_t *__restrict__ kq, KvTables kt, float scale, const float *__restrict__ lse,
+                          const uint8_t *__restrict__ kq, KvTables kt, float scale, const float *__restrict__ stat,
                           float *__restrict__ weights)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -151,7 +155,7 @@ __global__ void __launch_bounds__(GA_THREADS)
                 if (c < cpl)
                     x = fmaf(to_f32<T>(q[t * q_stride + (int64_t)a * D + lane * cpl + c]) * (scale * LOG2E), kv[c], x);
             for (int f = 16; f > 0; f >>= 1) x += __shfl_xor_sync(FULL, x, f);
-            w += exp2f(x - lse[t * Hq + a]);
+            w = fmaf(exp2f(x - stat[2 * (t * Hq + a)]), stat[2 * (t * Hq + a) + 1], w);
         }
     if (lane == 0) weights[row] += w;
 }
@@ -162,7 +166,7 @@ size_t paged_attention_workspace(int64_t T, int Hq, int H, int D, int dtype, int
     if (paged_decode_takes(Hq, H, D, dtype, max_q, weights))
         return paged_decode_workspace(T, Hq, H, D, dtype, B, max_q, max_len, weights, num_sms);
     if (D == 64 || D == 128) return paged_chunk_workspace(T, Hq, H, D, dtype, B, max_len, weights, num_sms);
-    return weights ? (size_t)T * Hq * sizeof(float) : 0;
+    return weights ? (size_t)T * Hq * 2 * sizeof(float) : 0;
 }
 
 template <typename T, int BITS>
@@ -170,13 +174,13 @@ static cudaError_t launch_paged_attention_t(const PagedAttnArgs &a)
 {
     const Paged p{a.start, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, a.max_q, a.max_len, a.err};
     const T *q = static_cast<const T *>(a.q);
-    float *lse = a.weights ? static_cast<float *>(a.ws) : nullptr;
+    float *stat = a.weights ? static_cast<float *>(a.ws) : nullptr;
     paged_attention_general<T, BITS><<<(unsigned)(a.T * a.Hq), GA_THREADS, 0, a.stream>>>(
-        q, a.q_stride, p, a.Hq, a.H, a.D, a.kq, a.vq, a.kt, a.scale, static_cast<T *>(a.out), lse);
+        q, a.q_stride, p, a.Hq, a.H, a.D, a.kq, a.vq, a.kt, a.scale, static_cast<T *>(a.out), stat);
     if (a.weights)
         paged_weights_general<T, BITS>
             <<<(unsigned)((int64_t)((a.max_len + GA_WARPS - 1) / GA_WARPS) * a.B * a.H), GA_THREADS, 0, a.stream>>>(
-                q, a.q_stride, p, a.Hq, a.H, a.D, a.kq, a.kt, a.scale, lse, a.weights);
+                q, a.q_stride, p, a.Hq, a.H, a.D, a.kq, a.kt, a.scale, stat, a.weights);
     return cudaGetLastError();
 }
 

@@ -6,6 +6,7 @@
 // not passed, and call the C ABI (whose addresses bind() is given).  They return the call's status; rptq.py raises.
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -77,13 +78,26 @@ struct Args {
               (t->numel() == 0 || (t->stride(2) == 1 && t->stride(1) == shape[2]));
         return ok ? t->data_ptr() : nullptr;
     }
-    rptq_stream_t stream()
+};
+
+// The stream of a call: the current one for None, else the given handle, which is then the current one while this lives,
+// so that what is allocated for the call belongs to it.
+struct Stream {
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    rptq_stream_t handle = nullptr;
+    Stream(Args &a, PyObject *o)
     {
-        PyObject *o = next();
-        if (o == Py_None) return (rptq_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-        void *p = PyLong_AsVoidPtr(o);
-        if (p == nullptr && PyErr_Occurred()) throw python_error();
-        return (rptq_stream_t)p;
+        if (!a.ok) return;
+        const auto dev = (c10::DeviceIndex)a.dev;
+        if (o != Py_None) {
+            void *p = PyLong_AsVoidPtr(o);
+            if (p == nullptr && PyErr_Occurred()) throw python_error();
+            guard.reset_stream(p == nullptr ? c10::cuda::getDefaultCUDAStream(dev)
+                                            : c10::cuda::getStreamFromExternal((cudaStream_t)p, dev));
+            handle = (rptq_stream_t)p;
+        } else {
+            handle = (rptq_stream_t)c10::cuda::getCurrentCUDAStream(dev).stream();
+        }
     }
 };
 
@@ -178,11 +192,11 @@ PyObject *append(PyObject *, PyObject *const *v, Py_ssize_t n)
          *table = a.dense<int32_t>(t[4], at::kInt, {p.B, p.max_pages});
     auto *kp = t[0] ? a.dense<uint8_t>(t[5], at::kByte, p.shape) : nullptr, *vp = t[1] ? a.dense<uint8_t>(t[6], at::kByte, p.shape) : nullptr;
     auto *sums = a.dense<float>(weights, at::kFloat, {p.n_pages, p.H, p.P});
-    const rptq_stream_t stream = a.ok ? a.stream() : nullptr;
+    const Stream stream(a, v[15]);
     if (!a.ok) return status(RPTQ_ERR_INVALID_ARG);
     return status(f_append(k, w, dtype_code(ty), T, (int)p.H, (int)p.D, row_stride(*x), start, lens, (int)p.B, table,
                            (int)p.max_pages, p.n_pages, (int)p.P, ck.cluster, ck.scale, ck.zero, cv.cluster, cv.scale, cv.zero,
-                           (int)(t[0] ? ck.g : cv.g), bits, kp, vp, sums, stream));
+                           (int)(t[0] ? ck.g : cv.g), bits, kp, vp, sums, stream.handle));
     END_HANDLE_TH_ERRORS
 }
 
@@ -202,6 +216,7 @@ PyObject *dequant(PyObject *, PyObject *const *v, Py_ssize_t n)
     const Pool p(a, t[0], t[1], bits);
     a.ok = a.ok && (given ? given->dim() == 3 && dtype_code(given->scalar_type()) >= 0 : T >= 0 && code >= 0 && code <= 2);
     if (!a.ok) return status_and(RPTQ_ERR_INVALID_ARG, at::Tensor());
+    const Stream stream(a, v[11]);
     at::Tensor out = given ? *given
                            : at::empty({T, p.H, p.D}, t[0]->options().dtype(code == RPTQ_F32   ? at::kFloat
                                                                            : code == RPTQ_F16 ? at::kHalf
@@ -213,10 +228,9 @@ PyObject *dequant(PyObject *, PyObject *const *v, Py_ssize_t n)
     auto *start = a.dense<int32_t>(t[2], at::kInt, {p.B + 1}), *begin = a.dense<int32_t>(t[3], at::kInt, {p.B}),
          *table = a.dense<int32_t>(t[1], at::kInt, {p.B, p.max_pages});
     void *o = a.dense(&out, out.scalar_type(), {T, p.H, p.D});
-    const rptq_stream_t stream = a.ok ? a.stream() : nullptr;
     if (!a.ok) return status_and(RPTQ_ERR_INVALID_ARG, at::Tensor());
     return status_and(f_dequant(pages, (int)p.H, (int)p.D, bits, start, begin, (int)p.B, table, (int)p.max_pages, p.n_pages,
-                                (int)p.P, T, c.cluster, c.scale, c.zero, (int)c.g, o, dtype_code(out.scalar_type()), stream),
+                                (int)p.P, T, c.cluster, c.scale, c.zero, (int)c.g, o, dtype_code(out.scalar_type()), stream.handle),
                       out);
     END_HANDLE_TH_ERRORS
 }
@@ -250,6 +264,7 @@ PyObject *attention(PyObject *, PyObject *const *v, Py_ssize_t n)
     auto *kp = a.dense<uint8_t>(t[4], at::kByte, p.shape), *vp = a.dense<uint8_t>(t[5], at::kByte, p.shape);
     auto *sums = a.dense<float>(weights, at::kFloat, {p.n_pages, p.H, p.P});
     if (!a.ok || t[5] == nullptr) return status_and(RPTQ_ERR_INVALID_ARG, at::Tensor());
+    const Stream stream(a, v[19]);
     at::Tensor out = given ? *given : at::empty({T, Hq, p.D}, q->options());
     void *o = a.dense(&out, ty, {T, Hq, p.D});
     const size_t bytes = f_workspace(T, (int)Hq, (int)p.H, (int)p.D, dt, (int)p.B, max_q, max_len, weights != nullptr);
@@ -264,11 +279,10 @@ PyObject *attention(PyObject *, PyObject *const *v, Py_ssize_t n)
         ws = own.data_ptr();
         ws_bytes = bytes;
     }
-    const rptq_stream_t stream = a.ok ? a.stream() : nullptr;
     if (!a.ok) return status_and(RPTQ_ERR_INVALID_ARG, at::Tensor());
     return status_and(f_attention(qp, dt, T, (int)Hq, (int)p.H, (int)p.D, row_stride(*q), start, lens, (int)p.B, max_q, max_len, table,
                                   (int)p.max_pages, p.n_pages, (int)p.P, kp, vp, ck.cluster, ck.scale, ck.zero, cv.cluster,
-                                  cv.scale, cv.zero, (int)ck.g, bits, (float)scale, o, sums, ws, ws_bytes, stream),
+                                  cv.scale, cv.zero, (int)ck.g, bits, (float)scale, o, sums, ws, ws_bytes, stream.handle),
                       out);
     END_HANDLE_TH_ERRORS
 }
@@ -295,13 +309,13 @@ PyObject *evict(PyObject *, PyObject *const *v, Py_ssize_t n)
     auto *lens = a.dense<int32_t>(t[3], at::kInt, {p.B}), *table = a.dense<int32_t>(t[4], at::kInt, {p.B, p.max_pages});
     int st = RPTQ_ERR_INVALID_ARG;
     if (a.ok) {
+        const Stream stream(a, v[11]);
         new_lens = new_given ? *new_given : at::empty({p.B}, t[3]->options());
         kept = kept_given ? *kept_given : at::empty({p.B, p.H, room}, t[3]->options());
         auto *nl = a.dense<int32_t>(&new_lens, at::kInt, {p.B}), *kt = a.dense<int32_t>(&kept, at::kInt, {p.B, p.H, room});
-        const rptq_stream_t stream = a.ok ? a.stream() : nullptr;
         if (a.ok)
             st = f_evict(kp, vp, sums, (int)p.B, (int)p.H, (int)p.D, bits, lens, table, (int)p.max_pages, p.n_pages, (int)p.P,
-                         (int)max_len, budget, recent, nl, kt, stream);
+                         (int)max_len, budget, recent, nl, kt, stream.handle);
     }
     PyObject *r = PyTuple_New(3);
     PyTuple_SET_ITEM(r, 0, status(st));

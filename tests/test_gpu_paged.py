@@ -370,6 +370,59 @@ def test_captured_step_follows_the_tables():
         check_attention(c, q.cpu(), out, "bf16", weights=d["w"], k=k, v=v)
 
 
+@pytest.mark.parametrize("n", [1, 150])
+def test_calls_on_other_streams(n):
+    """Two problems on two streams at once, each with its own workspace and outputs from the binding, while the current stream
+    reuses what the allocator hands it; results equal the ones alone."""
+    cs = [Case(4, 128, 3, 64, [n, n], [900, 700], seed=33 + i, sums=True) for i in range(2)]
+    qs = [c.queries(8, "bf16").to(DEV) for c in cs]
+    alone, sums = [], []
+    for c, q in zip(cs, qs):
+        alone.append(c.attend(q).clone())
+        sums.append(c.d["w"].clone())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for turn in range(5):
+        for c in cs:
+            c.d["w"].copy_(torch.from_numpy(c.w0))
+        torch.cuda.synchronize()
+        outs = []
+        for c, q, s in zip(cs, qs, streams):
+            outs.append(c.attend(q, stream=s))  # the current stream stays what it is
+            for _ in range(3):
+                torch.full((1 << 20,), float(turn), device=DEV)
+        torch.cuda.synchronize()
+        for i, c in enumerate(cs):
+            assert torch.equal(outs[i], alone[i]) and torch.equal(c.d["w"], sums[i])
+
+
+def test_two_graphs_share_a_workspace_in_turn():
+    """A decode step and a chunk captured apart with one workspace between them, replayed in turn on one stream."""
+    c = Case(2, 128, 4, 16, [1, 1], [500, 333], seed=35, sums=True)
+    k = Case(2, 128, 4, 16, [140, 3], [500, 333], seed=35, sums=True)
+    ws = torch.empty(max(rptq.rptq_kv_paged_attention_workspace_size(x.T, 4, 2, 128, torch.float16, 2, x.max_q, x.max_len, True)
+                         for x in (c, k)), dtype=torch.uint8, device=DEV)
+    graphs = []
+    for x in (c, k):
+        q = x.queries(4, "f16").to(DEV)
+        want = x.attend(q).clone()
+        sums = x.d["w"].clone()
+        out = torch.empty_like(q)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.attend(q, out=out, workspace=ws)
+        graphs.append((x, g, out, want, sums, q))  # q stays alive: the graph reads it
+    for _ in range(3):
+        for x, g, out, want, sums, _ in graphs:
+            x.d["w"].copy_(torch.from_numpy(x.w0))
+            out.zero_()
+            ws.fill_(0xA5)  # garbage: nothing of the last call may be counted on
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(x.d["w"], sums)
+
+
 # ---- what only the device can see ------------------------------------------------------------------
 @pytest.mark.parametrize("n", [1, 140])
 def test_bad_tables_are_reported_and_left_out(n):

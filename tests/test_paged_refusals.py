@@ -71,7 +71,8 @@ def test_shapes_every_call_refuses(lib, call, bad, status):
     (_attend, dict(max_q=-1), INVALID), (_attend, dict(scale=-1.0), INVALID), (_attend, dict(scale=float("nan")), INVALID),
     (_attend, dict(scale=float("inf")), INVALID), (_attend, dict(stride=255), INVALID), (_attend, dict(stride=260), INVALID),
     (_attend, dict(q=None), INVALID), (_attend, dict(out=P(16 * 1024 + 4)), INVALID), (_attend, dict(zk=None), INVALID),
-    (_attend, dict(T=1 << 31), UNSUPPORTED), (_attend, dict(w=A, ws=None), WORKSPACE), (_attend, dict(w=A, ws_bytes=8), WORKSPACE),
+    (_attend, dict(T=1 << 31), UNSUPPORTED), (_attend, dict(T=1 << 30), UNSUPPORTED),  # T Hq
+    (_attend, dict(w=A, ws=None), WORKSPACE), (_attend, dict(w=A, ws_bytes=8), WORKSPACE),
     (_attend, dict(w=A, ws=P(16 * 1024 + 8)), WORKSPACE),
     (_evict, dict(budget=0), INVALID), (_evict, dict(recent=-1), INVALID), (_evict, dict(recent=9), INVALID),
     (_evict, dict(max_len=49), INVALID), (_evict, dict(w=None), INVALID), (_evict, dict(kept=None), INVALID),
