@@ -8,7 +8,7 @@
 //     x_p = scale sum_d q_d s_d (code_pd - z_d):  the z part is the same for every position of a row and
 //           drops out of the softmax;  q'_d = q_d s_d goes in as fp16, scaled by a power of two per row
 //           that puts its largest |q'| in [2^14, 2^15);
-//     out_d = s_d (sum_p w_p code_pd / sum_p w_p - z_d).
+//     out_d = s_d (sum_p w_p (code_pd - c_d) / sum_p w_p - (z_d - c_d)),  c_d = 0, or the code nearest to z_d.
 // Where the result must be good to fp32 (fp32 queries; running sums of weights, which are fp32 and
 // long-lived) an operand is split into two fp16 parts, 22 bits together; elsewhere q' and w carry fp16's
 // 11 bits (an error of 2^-11 at most, below the output's own rounding to bf16 or fp16).
@@ -85,13 +85,11 @@ __device__ __forceinline__ uint32_t code_up_plus(uint32_t v, uint32_t c)
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x74007400u), "r"(c));
     return r;
 }
-// two codes at bit positions P0 and P1, times 2^14, about their middle
-template <int P0, int P1, int MID>
-__device__ __forceinline__ uint32_t code_about_mid(uint32_t v)
-{
-    constexpr uint32_t E = (MID == 8 ? 3 : 2) - 10 + 15;  // MID 2^(pos - 10) is a power of two: its exponent field less pos
-    return code_up_plus(v, (0x8000u | (E + P0) << 10) | (0x8000u | (E + P1) << 10) << 16);
-}
+// The code nearest to a channel's zero point: V's codes enter the precise products less this one, so that a value's error
+// is relative to the value (zero stays exactly zero) and not to the step times the code.
+__device__ __forceinline__ int zero_code(int z, int qmax) { return min(max(z, 0), qmax); }
+// -c 2^(pos - 10), as code_up_plus takes it, for a code c
+__device__ __forceinline__ float code_offset(int c, int pos) { return -(float)c * __uint_as_float((uint32_t)(117 + pos) << 23); }
 __device__ __forceinline__ uint32_t lds32(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
 // ---- K: one thread's D / 4 consecutive codes of a row as D / 8 pairs --------------------------------------
@@ -171,15 +169,6 @@ struct KPairs {
         read(a, t, w);
         expand(w, x);
     }
-    // expanded pairs to 2^(pos - 10) (code - mid): exact normal numbers
-    template <int I = 0>
-    __device__ __forceinline__ static void about_mid(uint32_t (&x)[N])
-    {
-        if constexpr (I < N) {
-            x[I] = code_about_mid<pos(I, 0), pos(I, 1), 1 << (BITS - 1)>(x[I]);
-            about_mid<I + 1>(x);
-        }
-    }
     __device__ __forceinline__ static void window(uint32_t w, uint32_t *x)
     {
         x[0] = w & 0x001C0007u;
@@ -204,7 +193,7 @@ struct PagedAttnDev {
     int splits;
     float *part, *ml, *scores;
     float *stat;  // [T Hq, 2] maximum and reciprocal of the sum of each row, for the running sums of a chunk
-    float mid;    // what the codes of V have had taken off in `part`
+    int centred;  // V's codes in `part` have had zero_code() taken off (their largest code; 0: nothing)
 };
 
 // few rows to a K/V head (kv_paged_decode.cu)

@@ -10,10 +10,13 @@
 // The two tiles share K and V and take turns on the tensor core: one's softmax runs while the other's
 // products do.  The codes come from global memory a tile ahead, are masked in place (kv_paged_attn.cuh) and
 // brought to small exact fp16 numbers by one fused multiply-add per two: K's relative to position 0's codes (a shift of all
-// scores of a row, which the softmax does not see; S then has the size of the scores' spread), V's about their middle.
+// scores of a row, which the softmax does not see; S then has the size of the scores' spread), V's relative to the code
+// nearest to the channel's zero point.
 // Queries come from a first kernel as finished operand tiles, already scaled (q' = q s) and in the 128-byte swizzle.
-// Where the scores must be good to fp32 (fp32 queries, or running sums of weights), q' has two fp16 parts on one
-// grid and S takes two products; fp32 outputs have W in two parts as well.
+// Where the scores must be good to fp32 (fp32 queries, or running sums of weights), q' has three parts and S takes three
+// products, in two accumulators of 64 positions.  fp32 outputs have W in two parts as well, and the products of a tile are
+// added to O by the softmax's threads: the tensor core's own additions are cut off at the accumulator's last bit, and the
+// many of a long row would all err to the same side (4e-6 after 1287 positions, measured).
 //
 // Running sums: a third kernel goes over the positions again with the rows' maxima and sums known: tiles of 128
 // positions are the row operand, S^T = K q'^T, so that a thread owns a position and adds its weights in registers,
@@ -32,7 +35,10 @@ constexpr int CH_PROD0 = CH_SOFT_WARPS, CH_MMA0 = CH_PROD0 + CH_PROD_WARPS;
 constexpr int CH_THREADS = 32 * (CH_MMA0 + 4);  // whole warpgroups: registers are moved between them
 constexpr uint32_t CH_SLAB = CH_M * 128;  // 128 rows of 64 fp16
 // Weights are held as 2^y, y = x - m + CH_PSHIFT for a reference m that follows the running maximum (it moves when
-// some y passes CH_YMAX); fp16's smallest step is then 2^-(24 + CH_PSHIFT) of a weight at the reference.
+// some y passes CH_YMAX); fp16's smallest step is then 2^-(24 + CH_PSHIFT) of a weight at the reference.  Outputs of 16 bits
+// take the largest score itself for m: its weight is a power of two and has no rounding.  fp32 outputs, whose weights have
+// two parts, take an integer: CH_PSHIFT - m and the factors are exact.  Running sums beside outputs of 16 bits need both, so
+// there the shift is 0 and y = x - m rounds once.
 constexpr float CH_PSHIFT = 5.f, CH_YMAX = 15.f;
 
 // 2^y of two exponents on the FMA pipe: y = n + f with n the nearest integer (the sum with 1.5 * 2^23 holds it in its
@@ -127,7 +133,8 @@ __device__ __forceinline__ void load_row(const void *p, int dtype, int64_t at, f
 
 // ---- the queries as operand tiles -----------------------------------------------------------------------
 // One CTA per (tile slot, head), a warp to a row.  PARTS = 1: fp16 of q' scaled so that the row's largest is in
-// [2^14, 2^15); 2: integers of 11 bits, the second 2^-11 of the first's unit and stored so.
+// [2^14, 2^15).  3: integers of 11 bits on grids of 2^-11 of each other, relative to the row's largest; the second is
+// stored as an integer (it has an accumulator of its own), the third in the second's unit.
 constexpr int CQ_THREADS = 256;
 template <int BITS, int D, int PARTS>
 __global__ void __launch_bounds__(CQ_THREADS)
@@ -199,9 +206,11 @@ __global__ void __launch_bounds__(CQ_THREADS)
                 float f = v[u][k] * up;
                 const float g = PARTS == 1 ? f : rintf(f);
                 *reinterpret_cast<__half *>(tile + sw) = __float2half_rn(g * down);
-                if (PARTS == 2) {  // on the grid of 2^-11: exact in fp16
-                    f = rintf((f - g) * 2048.f) * 0x1p-11f;
-                    *reinterpret_cast<__half *>(tile + (D / 64) * CH_SLAB + sw) = __float2half_rn(f * down);
+                if (PARTS > 1) {  // (every difference and product is exact)
+                    f = (f - g) * 2048.f;
+                    const float g2 = rintf(f), g3 = rintf((f - g2) * 2048.f) * 0x1p-11f;
+                    *reinterpret_cast<__half *>(tile + (D / 64) * CH_SLAB + sw) = __float2half_rn(g2 * down);
+                    *reinterpret_cast<__half *>(tile + 2 * (D / 64) * CH_SLAB + sw) = __float2half_rn(g3 * down);
                 }
             }
         }
@@ -212,7 +221,7 @@ __global__ void __launch_bounds__(CQ_THREADS)
 }
 
 // ---- expansion of the codes -----------------------------------------------------------------------------
-// A producer thread (0-127) has one quarter of every 32nd row of a tile.  The eight lanes of one 16-byte store phase
+// A producer thread (0-127) has one quarter of every 32nd row of a tile of 64 or 128.  The eight lanes of one 16-byte store phase
 // write eight different 16-byte columns of the swizzled tile: D = 128: two quarters (of one slab) of four rows;
 // D = 64: four quarters of two rows.
 template <int D>
@@ -223,55 +232,57 @@ __device__ __forceinline__ void chunk_share(int pt, int &r0, int &t)
     else
         t = pt & 3, r0 = pt >> 2;
 }
-// The pages of its four rows of the tile at pos0, as the table has them; page 0 for one outside the pool.
-__device__ __forceinline__ void chunk_pages(const Paged &p, int b, int pos0, int L, int r0, int (&ids)[4])
+// The pages of its N rows of the tile (of 32 N) at pos0, as the table has them; page 0 for one outside the pool.
+template <int N>
+__device__ __forceinline__ void chunk_pages(const Paged &p, int b, int pos0, int L, int r0, int (&ids)[N])
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
         const int pos = pos0 + r0 + 32 * i;
         ids[i] = pos < L ? p.table[(int64_t)b * p.max_pages + (pos >> p.shift)] : 0;
     }
 }
-__device__ __forceinline__ void chunk_check(const Paged &p, int (&ids)[4])
+template <int N>
+__device__ __forceinline__ void chunk_check(const Paged &p, int (&ids)[N])
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N; ++i)
         if (ids[i] < 0 || ids[i] >= p.n_pages) {
             raise_error(p.err, RPTQ_DEVERR_PAGE);
             ids[i] = 0;
         }
 }
-// its four rows' packed words ...
-template <int BITS, int D>
+// its rows' packed words ...
+template <int BITS, int D, int N>
 struct ChunkCodes {
     using KP = KPairs<BITS, D>;
-    uint32_t w[4][KP::NW];
+    uint32_t w[N][KP::NW];
     // rows r0, r0 + 32, ... of the tile at pos0, in pages `ids`; zeros past the sequence
-    __device__ __forceinline__ void read(const uint8_t *pages, const Paged &p, const int (&ids)[4], int H, int h, int pos0, int L,
+    __device__ __forceinline__ void read(const uint8_t *pages, const Paged &p, const int (&ids)[N], int H, int h, int pos0, int L,
                                          int r0, int t)
     {
         constexpr int RB = D * BITS / 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < N; ++i) {
             const int pos = pos0 + r0 + 32 * i;
 #pragma unroll
             for (int k = 0; k < KP::NW; ++k) w[i][k] = 0;
             if (pos < L) KP::read(pages + (paged_row(ids[i], H, h, p.shift) + (pos & ((1 << p.shift) - 1))) * RB, t, w[i]);
         }
     }
-    // ... to shared memory: fp16 of D / 64 slabs of [128 rows, 128 bytes] in the 128-byte swizzle
+    // ... to shared memory: fp16 of D / 64 slabs of [32 N rows, 128 bytes] in the 128-byte swizzle
     template <typename F>
     __device__ __forceinline__ void write(uint32_t tile, int r0, int t, F shape) const
     {
         constexpr int PIECES = KP::N / 4;  // 16-byte pieces of a quarter
         const int slab = t * PIECES / 8, c0 = t * PIECES % 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < N; ++i) {
             uint32_t x[KP::N];
             KP::expand(w[i], x);
             shape(x);
             const int r = r0 + 32 * i;
-            const uint32_t row = tile + slab * CH_SLAB + r * 128;
+            const uint32_t row = tile + slab * N * 4096 + r * 128;
 #pragma unroll
             for (int j = 0; j < PIECES; ++j) {
                 const uint32_t at = row + (((c0 + j) ^ (r & 7)) << 4);
@@ -295,12 +306,15 @@ __device__ __forceinline__ void chunk_reference(const PagedAttnDev &a, int b, in
 }
 
 // ---- attention --------------------------------------------------------------------------------------------
-template <int D, int QP>
+template <int D, int QP>  // QP: parts of q', 1 or 3
 struct ChunkShape {
     static constexpr int SLABS = D / 64;
-    static constexpr uint32_t KV = SLABS * CH_SLAB;           // a K or V tile
-    static constexpr uint32_t QT = QP * SLABS * CH_SLAB;      // a query tile
-    static constexpr int STAGES = QP == 2 && D == 128 ? 1 : 2;  // what 227 KB leave
+    // Positions of a tile.  With more than one part, S has two accumulators (the sums of the first part, and those of the
+    // others, are exact or nearly so by themselves; in one they would lose what is below 2^-24 of the larger): half as many.
+    static constexpr int KEYS = QP == 1 ? 128 : 64;
+    static constexpr uint32_t KV_SLAB = KEYS * 128, KV = SLABS * KV_SLAB;  // a K or V tile
+    static constexpr uint32_t QT = QP * SLABS * CH_SLAB;                   // a query tile
+    static constexpr int STAGES = QP == 3 && D == 128 ? 1 : 2;             // what 227 KB leave
     static constexpr uint32_t SMEM = 1024 + 2 * QT + 2 * STAGES * KV;
     static constexpr uint32_t O_COL = 256;  // O of tile g at O_COL + g * D
 };
@@ -311,11 +325,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
 {
     using S = ChunkShape<D, QP>;
     using KP = KPairs<BITS, D>;
-    constexpr int ST = S::STAGES;
+    constexpr int ST = S::STAGES, KEYS = S::KEYS;
+    constexpr float SHIFT = QP == 3 && PP == 1 ? 0.f : CH_PSHIFT;  // of the weights' exponents (see CH_PSHIFT)
+    constexpr int HALVES = D / 64;  // PP = 2: a tile's product, 64 channels at a time, lies where S's second accumulator was
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[4 * 2 + 3 * 2 + 2];
+    __shared__ __align__(8) uint64_t bars[4 * 2 + 4 * 2 + 2];
     __shared__ uint32_t tmem_slot;
     __shared__ float s_sv[D], s_zv[D];
+    __shared__ int s_zc[D];
     const PagedAttnDev &a = c.a;
     const Paged &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -336,14 +353,14 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     const int64_t qslot = (int64_t)h * c.slots + chunk_base(p, b, a.G, CH_M) + 2 * block;
     // tiles of positions: those that the last row sees, this part's share
     const int vis = max(0, L - n + (row0 + rows - 1) / a.G + 1);
-    const int all = (vis + CH_KEYS - 1) / CH_KEYS;
+    const int all = (vis + KEYS - 1) / KEYS;
     const int j0 = (int)((int64_t)all * split / a.splits), j1 = (int)((int64_t)all * (split + 1) / a.splits);
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t sQ = base, sK = base + 2 * S::QT, sV = sK + ST * S::KV;
     const uint32_t bar = smem_u32(bars);
     const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_empty = bar + 48;  // [2] each
-    const uint32_t s_full = bar + 64, p_full = bar + 80, o_done = bar + 96, q_full = bar + 112, drain = bar + 120;
+    const uint32_t s_full = bar + 64, p_full = bar + 80, o_done = bar + 96, o_free = bar + 112, q_full = bar + 128, drain = bar + 136;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(k_full + 8 * i, 32 * CH_PROD_WARPS);
@@ -353,6 +370,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, CH_M);
             mbar_init(o_done + 8 * i, 1);
+            mbar_init(o_free + 8 * i, CH_M);
         }
         mbar_init(q_full, 1);
         mbar_init(drain, 1);
@@ -361,7 +379,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     for (int d = tid; d < D; d += CH_THREADS) {
         const int k = cluster_of(a.kt.cv, h * D + d, a.kt.g, p.err);
         s_sv[d] = a.kt.sv[k];
-        s_zv[d] = (float)a.kt.zv[k] - (float)(1 << (BITS - 1));
+        const int z = a.kt.zv[k], zc = zero_code(z, (1 << BITS) - 1);
+        s_zv[d] = (float)(z - zc);
+        s_zc[d] = zc;
     }
     if (warp == CH_MMA0) tc_alloc(smem_u32(&tmem_slot), 512);
     tc_fence_before();
@@ -377,7 +397,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         const bool live = g < nact && row < R;
         if (g < nact) {
             const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-            const uint32_t tS = tmem + lanes + (uint32_t)g * CH_KEYS, tO = tmem + lanes + S::O_COL + (uint32_t)g * D;
+            const uint32_t tS = tmem + lanes + (uint32_t)g * CH_M, tO = tmem + lanes + S::O_COL + (uint32_t)g * D;
             const float cx = c.cx[(qslot + g) * CH_M + r];
             const int vrow = live ? L - n + row / a.G + 1 : 0;                    // visible positions
             const int vmin = L - n + (row0 + g * CH_M + 32 * quad) / a.G + 1;     // of the warp's first row
@@ -388,8 +408,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 ok = __all_sync(FULL, mbar_wait_bounded(s_full + 8 * g, (j - j0) & 1, p.err));
                 if (!ok) break;
                 tc_fence_after();
-                const int pos0 = j * CH_KEYS;
-                const bool whole = pos0 + CH_KEYS <= vmin;
+                const int pos0 = j * KEYS;
+                const bool whole = pos0 + KEYS <= vmin;
                 float top = -INFINITY;
                 uint32_t v[4][32];  // the row of S
 #pragma unroll
@@ -397,26 +417,31 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 tc_wait_ld();
 #pragma unroll
                 for (int q4 = 0; q4 < 4; ++q4) tc_loaded(v[q4]);
+                if (QP > 1) {  // the first part's sums and the others'
+#pragma unroll
+                    for (int k = 0; k < KEYS; ++k)
+                        v[k / 32][k % 32] = __float_as_uint(fmaf(__uint_as_float(v[2 + k / 32][k % 32]), 0x1p-11f, __uint_as_float(v[k / 32][k % 32])));
+                }
                 if (!whole) {
 #pragma unroll
-                    for (int k = 0; k < CH_KEYS; ++k)
+                    for (int k = 0; k < KEYS; ++k)
                         if (pos0 + k >= vrow) v[k / 32][k % 32] = 0xff800000u;  // -inf (cx > 0)
                 }
 #pragma unroll
-                for (int k = 0; k < CH_KEYS; k += 2)
+                for (int k = 0; k < KEYS; k += 2)
                     top = max3f(top, __uint_as_float(v[k / 32][k % 32]), __uint_as_float(v[k / 32][k % 32 + 1]));
                 // cx > 0, so the largest score is cx * the largest S
                 const float ytop = fmaf(top, cx, off);
+                float f = 1.f;
                 if (__any_sync(FULL, ytop > CH_YMAX)) {
-                    float f = 1.f;
-                    if (live && ytop > CH_PSHIFT) {
-                        const float mn = top * cx;
+                    if (live && ytop > SHIFT) {
+                        const float mn = PP == 1 ? top * cx : ceilf(top * cx);
                         f = ex2(m - mn);
                         m = mn;
-                        off = CH_PSHIFT - mn;
+                        off = SHIFT - mn;
                         l2 = mul2(l2, mk2(f, f));
                     }
-                    if (j > j0) {  // O of the tiles so far (its products are complete: the scores waited for them)
+                    if (PP == 1 && j > j0) {  // O of the tiles so far (its products are complete: the scores waited for them)
 #pragma unroll 1
                         for (int q8 = 0; q8 < D / 8; ++q8) {
                             uint32_t x[8];
@@ -429,12 +454,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 }
                 const f32x2 cx2 = mk2(cx, cx), off2 = mk2(off, off);
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
+                for (int q4 = 0; q4 < KEYS / 32; ++q4) {
                     uint32_t w[16], w2[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const f32x2 y = fma2(mk2(__uint_as_float(v[q4][2 * k]), __uint_as_float(v[q4][2 * k + 1])), cx2, off2);
-                        // (exact sums of weights, QP = 2, stay with the finer function)
+                        // (precise weights stay with the finer function)
                         const f32x2 e = QP == 1 && k % CH_POLY == CH_POLY - 1 ? exp2_poly(y) : mk2(ex2(lo2(y)), ex2(hi2(y)));
                         l2 = add2(l2, e);
                         w[k] = half2_bits(lo2(e), hi2(e));
@@ -450,13 +475,40 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 tc_wait_st();
                 tc_fence_before();
                 lin_arrive(p_full + 8 * g);
+                if constexpr (PP == 2) {  // O = f O + this tile's product
+                    for (int hf = 0; hf < HALVES && ok; ++hf) {
+                        ok = __all_sync(FULL, mbar_wait_bounded(o_done + 8 * g, ((j - j0) * HALVES + hf) & 1, p.err));
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int q4 = 0; q4 < 2; ++q4) {
+                            uint32_t x[32], o[32];
+                            tc_ld32_async(tS + 64 + 32 * q4, x);
+                            if (j > j0) tc_ld32_async(tO + 64 * hf + 32 * q4, o);
+                            tc_wait_ld();
+                            tc_loaded(x);
+                            if (j > j0) {
+                                tc_loaded(o);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    x[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), f, __uint_as_float(x[k])));
+                            }
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) tc_st16(tO + 64 * hf + 32 * q4 + 16 * k, reinterpret_cast<uint32_t(&)[16]>(x[16 * k]));
+                        }
+                        tc_wait_st();
+                        tc_fence_before();
+                        lin_arrive(o_free + 8 * g);
+                    }
+                }
             }
             // ---- the row's result ----
-            if (ok && j1 > j0) ok = mbar_wait_bounded(o_done + 8 * g, (j1 - j0 - 1) & 1, p.err);
+            if (PP == 1 && ok && j1 > j0) ok = mbar_wait_bounded(o_done + 8 * g, (j1 - j0 - 1) & 1, p.err);
             ok = __all_sync(FULL, ok);
             tc_fence_after();
             if (ok) {
-                const float l = (lo2(l2) + hi2(l2)) * 0x1p-5f;  // 2^-CH_PSHIFT
+                constexpr float UNSHIFT = SHIFT == 0.f ? 1.f : 0x1p-5f;  // 2^-SHIFT
+                const float l = (lo2(l2) + hi2(l2)) * UNSHIFT;
                 const bool sees = l > 0.f || l != l;
                 const int tok = row / a.G, jh = row - tok * a.G;
                 const int64_t orow = (int64_t)(s0 + tok) * a.Hq + h * a.G + jh;
@@ -476,7 +528,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                     for (int k = 0; k < 32; ++k) {
                         constexpr int Q = D / 4;  // columns of a quarter
                         const int i = k % Q / 2, e = k & 1;
-                        o[k / Q * Q + KP::code(i, e)] = __uint_as_float(v[k]) * ((float)(1 << (10 - KP::pos(i, e))) * 0x1p-5f);
+                        o[k / Q * Q + KP::code(i, e)] = __uint_as_float(v[k]) * ((float)(1 << (10 - KP::pos(i, e))) * UNSHIFT);
                     }
                     if (a.part != nullptr) {
                         float4 *dst = reinterpret_cast<float4 *>(a.part + ((int64_t)split * p.T * a.Hq + orow) * D + 32 * q4);
@@ -525,15 +577,19 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         chunk_share<D>(pt, r0, t);
         bool ok = true;
         if (j1 > j0) {
-            uint32_t ref[KP::N];
+            uint32_t ref[KP::N], zc[KP::N];  // what is taken off K's and V's codes
             chunk_reference<BITS, D>(a, b, h, t, ref);
-            ChunkCodes<BITS, D> kc, vc;
-            int ids[4];  // pages of the tile whose codes are read next: themselves read a tile before that
-            chunk_pages(p, b, j0 * CH_KEYS, L, r0, ids);
+#pragma unroll
+            for (int i = 0; i < KP::N; ++i)
+                zc[i] = half2_bits(code_offset(s_zc[t * (D / 4) + KP::code(i, 0)], KP::pos(i, 0)),
+                                   code_offset(s_zc[t * (D / 4) + KP::code(i, 1)], KP::pos(i, 1)));
+            ChunkCodes<BITS, D, KEYS / 32> kc, vc;
+            int ids[KEYS / 32];  // pages of the tile whose codes are read next: themselves read a tile before that
+            chunk_pages(p, b, j0 * KEYS, L, r0, ids);
             chunk_check(p, ids);
-            kc.read(a.kq, p, ids, a.H, h, j0 * CH_KEYS, L, r0, t);
-            vc.read(a.vq, p, ids, a.H, h, j0 * CH_KEYS, L, r0, t);
-            chunk_pages(p, b, (j0 + 1) * CH_KEYS, L, r0, ids);
+            kc.read(a.kq, p, ids, a.H, h, j0 * KEYS, L, r0, t);
+            vc.read(a.vq, p, ids, a.H, h, j0 * KEYS, L, r0, t);
+            chunk_pages(p, b, (j0 + 1) * KEYS, L, r0, ids);
             for (int j = j0; j < j1 && ok; ++j) {
                 const int i = j - j0, st = i % ST;
                 const uint32_t free_ph = ((uint32_t)(i / ST) & 1) ^ 1;
@@ -545,13 +601,16 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 fence_proxy_async_smem();
                 lin_arrive(k_full + 8 * st);
                 chunk_check(p, ids);
-                if (j + 1 < j1) kc.read(a.kq, p, ids, a.H, h, (j + 1) * CH_KEYS, L, r0, t);
+                if (j + 1 < j1) kc.read(a.kq, p, ids, a.H, h, (j + 1) * KEYS, L, r0, t);
                 if (!(ok = mbar_wait_bounded(v_empty + 8 * st, free_ph, p.err))) break;
-                vc.write(sV + st * S::KV, r0, t, [&](uint32_t(&x)[KP::N]) { KP::about_mid(x); });
+                vc.write(sV + st * S::KV, r0, t, [&](uint32_t(&x)[KP::N]) {
+#pragma unroll
+                    for (int k = 0; k < KP::N; ++k) x[k] = code_up_plus(x[k], zc[k]);
+                });
                 fence_proxy_async_smem();
                 lin_arrive(v_full + 8 * st);
-                if (j + 1 < j1) vc.read(a.vq, p, ids, a.H, h, (j + 1) * CH_KEYS, L, r0, t);
-                chunk_pages(p, b, (j + 2) * CH_KEYS, L, r0, ids);
+                if (j + 1 < j1) vc.read(a.vq, p, ids, a.H, h, (j + 1) * KEYS, L, r0, t);
+                chunk_pages(p, b, (j + 2) * KEYS, L, r0, ids);
             }
         }
         if (pt == 0) mbar_wait_bounded(q_full, 0, p.err);  // no copy may be in flight when the CTA ends
@@ -560,7 +619,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         //      tile's products run during the other's softmax ----
         reg_dec<64>();
         if (warp == CH_MMA0 && lane == 0) {
-            constexpr uint32_t qk = f16_idesc(CH_M, CH_KEYS), pv = f16_idesc(CH_M, D) | IDESC_B_MN;
+            constexpr uint32_t qk = f16_idesc(CH_M, KEYS), pv = f16_idesc(CH_M, D) | IDESC_B_MN;
             const int count = j1 - j0;
             auto scores = [&](int g, int st) {
                 const uint32_t q0 = sQ + g * S::QT;
@@ -568,8 +627,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 for (int part = 0; part < QP; ++part)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        tc_mma_f16_ss(tmem + (uint32_t)g * CH_KEYS, sw128_desc(q0 + (part * S::SLABS + kk / 4) * CH_SLAB) + 2 * (kk % 4),
-                                      sw128_desc(sK + st * S::KV + kk / 4 * CH_SLAB) + 2 * (kk % 4), qk, (part | kk) != 0);
+                        tc_mma_f16_ss(tmem + (uint32_t)(g * CH_M + (part > 0 ? KEYS : 0)),
+                                      sw128_desc(q0 + (part * S::SLABS + kk / 4) * CH_SLAB) + 2 * (kk % 4),
+                                      sw128_desc(sK + st * S::KV + kk / 4 * S::KV_SLAB) + 2 * (kk % 4), qk, part == 2 || kk != 0);
                 tc_commit(s_full + 8 * g);
             };
             bool ok = mbar_wait_bounded(q_full, 0, p.err);
@@ -580,17 +640,46 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             }
             for (int i = 0; i < count && ok; ++i) {
                 const int st = i % ST, st1 = (i + 1) % ST;
+                if constexpr (PP == 2) {
+                    constexpr uint32_t pv64 = f16_idesc(CH_M, 64) | IDESC_B_MN;
+                    for (int hf = 0; hf < HALVES && ok; ++hf)
+                        for (int g = 0; g < nact && ok; ++g) {
+                            const uint32_t tS = tmem + (uint32_t)g * CH_M;
+                            ok = hf == 0 ? mbar_wait_bounded(p_full + 8 * g, i & 1, p.err)
+                                         : mbar_wait_bounded(o_free + 8 * g, (i * HALVES + hf - 1) & 1, p.err);
+                            if (!ok) break;
+                            if (hf == 0 && g == 0 && !(ok = mbar_wait_bounded(v_full + 8 * st, (uint32_t)(i / ST) & 1, p.err))) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int part = 0; part < PP; ++part)
+#pragma unroll
+                                for (int kk = 0; kk < KEYS / 16; ++kk)
+                                    tc_mma_f16_ts(tS + 64, tS + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part,
+                                                  sw128_mn_desc(sV + st * S::KV + hf * S::KV_SLAB + kk * 2048, S::KV_SLAB), pv64, (part | kk) != 0);
+                            tc_commit(o_done + 8 * g);
+                            if (hf == HALVES - 1 && g == nact - 1) tc_commit(v_empty + 8 * st);
+                        }
+                    if (!ok || i + 1 == count) continue;
+                    if (!(ok = mbar_wait_bounded(k_full + 8 * st1, (uint32_t)((i + 1) / ST) & 1, p.err))) break;
+                    for (int g = 0; g < nact && ok; ++g) {
+                        if (!(ok = mbar_wait_bounded(o_free + 8 * g, (i * HALVES + HALVES - 1) & 1, p.err))) break;
+                        tc_fence_after();
+                        scores(g, st1);
+                        if (g == nact - 1) tc_commit(k_empty + 8 * st1);
+                    }
+                    continue;
+                }
                 for (int g = 0; g < nact && ok; ++g) {
-                    const uint32_t tS = tmem + (uint32_t)g * CH_KEYS, tO = tmem + S::O_COL + (uint32_t)g * D;
+                    const uint32_t tS = tmem + (uint32_t)g * CH_M, tO = tmem + S::O_COL + (uint32_t)g * D;
                     if (!(ok = mbar_wait_bounded(p_full + 8 * g, i & 1, p.err))) break;
                     if (g == 0 && !(ok = mbar_wait_bounded(v_full + 8 * st, (uint32_t)(i / ST) & 1, p.err))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int part = 0; part < PP; ++part)
 #pragma unroll
-                        for (int kk = 0; kk < CH_KEYS / 16; ++kk)
+                        for (int kk = 0; kk < KEYS / 16; ++kk)
                             tc_mma_f16_ts(tO, tS + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part,
-                                          sw128_mn_desc(sV + st * S::KV + kk * 2048, CH_SLAB), pv, i > 0 || (part | kk) != 0);
+                                          sw128_mn_desc(sV + st * S::KV + kk * 2048, S::KV_SLAB), pv, i > 0 || (part | kk) != 0);
                     tc_commit(o_done + 8 * g);
                     if (g == nact - 1) tc_commit(v_empty + 8 * st);
                     if (i + 1 == count) continue;
@@ -616,15 +705,17 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
 }
 
 // ---- running sums -------------------------------------------------------------------------------------------
-// One CTA per (sequence, head, 256 positions), all 512 tensor-memory columns: S^T of two tiles of 128 positions, twice.
-// Warps 0-3 and 4-7 take the row tiles in turn; a thread has one position of each tile, so that what it reads of a row
-// from shared memory (8 bytes for every lane: two clocks of the 128 bytes a clock) serves two weights.  Warp 8 issues the
-// MMAs, warp 9 the copies of the query tiles (two in flight).
-constexpr int CW_THREADS = 320, CW_TILES = 2;
+// One CTA per (sequence, head, 256 positions), all 512 tensor-memory columns: S^T of two tiles of 128 positions and half a
+// row tile, in two accumulators, twice.  Warps 0-3 take the first half of each row tile and warps 4-7 the second; a thread
+// has one position of each tile, so that what it reads of a row from shared memory (8 bytes for every lane: two clocks of the
+// 128 bytes a clock) serves two weights.  Warp 8 issues the
+// MMAs, warp 9 the copies of the query half tiles (three in flight).
+constexpr int CW_THREADS = 320, CW_TILES = 2, CW_ROWS = CH_M / 2, CW_STAGES = 3;
 template <int D>
 struct WeightShape {
-    static constexpr uint32_t QT = 2 * (D / 64) * CH_SLAB, KT = (D / 64) * CH_SLAB;
-    static constexpr uint32_t SMEM = 1024 + 2 * QT + CW_TILES * KT;
+    static constexpr uint32_t SLAB = CW_ROWS * 128, QT = 3 * (D / 64) * SLAB;  // of half a row tile
+    static constexpr uint32_t KT = (D / 64) * CH_SLAB;
+    static constexpr uint32_t SMEM = 1024 + CW_STAGES * QT + CW_TILES * KT;
 };
 template <int BITS, int D>
 __global__ void __launch_bounds__(CW_THREADS, 1)
@@ -633,10 +724,10 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     using S = WeightShape<D>;
     using KP = KPairs<BITS, D>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[9];
+    __shared__ __align__(8) uint64_t bars[2 * CW_STAGES + 5];
     __shared__ uint32_t tmem_slot;
-    __shared__ __align__(16) float2 s_row[2][2][CH_M];  // [group][turn][row]: cx, -(maximum + log2 of the sum)
-    __shared__ int s_vis[2][2][CH_M];                   // visible positions
+    __shared__ __align__(16) float2 s_row[2][2][CW_ROWS];  // [group][turn][row]: cx, -(maximum + log2 of the sum)
+    __shared__ int s_vis[2][2][CW_ROWS];                 // visible positions
     __shared__ float2 s_sum[CH_M];
     const PagedAttnDev &a = c.a;
     const Paged &p = a.p;
@@ -650,13 +741,15 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     const int64_t qslot = (int64_t)h * c.slots + chunk_base(p, b, a.G, CH_M);
     const int i0 = (int)((int64_t)max(0, first - (L - n)) * a.G / CH_M), i1 = (R + CH_M - 1) / CH_M;  // row tiles that see the block
 
-    const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u, sK = sQ + 2 * S::QT;
+    const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u, sK = sQ + CW_STAGES * S::QT;
     const uint32_t bar = smem_u32(bars);
-    const uint32_t q_full = bar, q_empty = bar + 16, s_full = bar + 32, s_free = bar + 48, drain = bar + 64;
+    const uint32_t q_full = bar, q_empty = q_full + 8 * CW_STAGES, s_full = q_empty + 8 * CW_STAGES, s_free = s_full + 16, drain = s_free + 16;
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < CW_STAGES; ++i) {
             mbar_init(q_full + 8 * i, 1);
             mbar_init(q_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 1);
             mbar_init(s_free + 8 * i, CH_M);
         }
@@ -671,7 +764,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         chunk_share<D>(tid & (CH_M - 1), r0, t);
         uint32_t ref[KP::N];
         chunk_reference<BITS, D>(a, b, h, t, ref);
-        ChunkCodes<BITS, D> kc;
+        ChunkCodes<BITS, D, CH_KEYS / 32> kc;
         chunk_pages(p, b, pos0, L, r0, ids);
         chunk_check(p, ids);
         kc.read(a.kq, p, ids, a.H, h, pos0, L, r0, t);
@@ -688,30 +781,32 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
 
     if (warp < 8) {
         const int quad = warp & 3, r = 32 * quad + lane;
-        const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)g * CW_TILES * CH_M;
+        const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)g * CW_TILES * CH_M;  // tile, part, row
         const int pos = first + r;  // and pos + 128
-        // the thread's row of tile i
+        // the row of tile i that the thread (of the group's first 64) fetches
         auto info = [&](int i, float2 &f, int &vis) {
-            const int row = i * CH_M + r;
+            const int row = i * CH_M + g * CW_ROWS + r;
             f = make_float2(0.f, -INFINITY);
             vis = 0;
-            if (i >= i1 || row >= R) return;
+            if (i >= i1 || r >= CW_ROWS || row >= R) return;
             const int tok = row / a.G, j = row - tok * a.G;
             const float2 st = *reinterpret_cast<const float2 *>(a.stat + 2 * ((int64_t)(s0 + tok) * a.Hq + h * a.G + j));
             // scores are relative to position 0's, so the maximum is small enough for the sum's log to be added to it
-            f = make_float2(c.cx[(qslot + i) * CH_M + r], st.y > 0.f ? log2f(st.y) - st.x : st.y == 0.f ? -INFINITY : st.y);
+            f = make_float2(c.cx[(qslot + i) * CH_M + g * CW_ROWS + r], st.y > 0.f ? log2f(st.y) - st.x : st.y == 0.f ? -INFINITY : st.y);
             vis = L - n + tok + 1;
         };
         f32x2 w = mk2(0.f, 0.f);  // of pos, pos + 128
         bool ok = true;
         float2 f;
         int vis;
-        info(i0 + g, f, vis);
-        for (int i = i0 + g, k = 0; i < i1; i += 2, ++k) {  // every warp takes every turn: the barrier counts them
-            s_row[g][k & 1][r] = f;
-            s_vis[g][k & 1][r] = vis;
+        info(i0, f, vis);
+        for (int i = i0, k = 0; i < i1; ++i, ++k) {  // every warp takes every turn: the barrier counts them
+            if (r < CW_ROWS) {
+                s_row[g][k & 1][r] = f;
+                s_vis[g][k & 1][r] = vis;
+            }
             asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
-            info(i + 2, f, vis);  // in flight during this turn
+            info(i + 1, f, vis);  // in flight during this turn
             ok = ok && __all_sync(FULL, mbar_wait_bounded(s_full + 8 * g, k & 1, p.err));
             if (!ok) continue;
             tc_fence_after();
@@ -720,17 +815,23 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             const int *seen = s_vis[g][k & 1];
             auto add = [&](auto all) {
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    uint32_t u[32], v[32];
+                for (int q4 = 0; q4 < CW_ROWS / 32; ++q4) {
+                    uint32_t u[32], v[32], u2[32], v2[32];
                     tc_ld32_async(tS + 32 * q4, u);
+                    tc_ld32_async(tS + CW_ROWS + 32 * q4, u2);
                     tc_ld32_async(tS + CH_M + 32 * q4, v);  // (of no use, and not used, without a second tile)
+                    tc_ld32_async(tS + CH_M + CW_ROWS + 32 * q4, v2);
                     tc_wait_ld();
                     tc_loaded(u);
+                    tc_loaded(u2);
                     tc_loaded(v);
+                    tc_loaded(v2);
 #pragma unroll
                     for (int q = 0; q < 32; ++q) {
                         const float2 s = rows[32 * q4 + q];
-                        const f32x2 y = fma2(mk2(__uint_as_float(u[q]), __uint_as_float(v[q])), mk2(s.x, s.x), mk2(s.y, s.y));
+                        const f32x2 x = fma2(mk2(__uint_as_float(u2[q]), __uint_as_float(v2[q])), mk2(0x1p-11f, 0x1p-11f),
+                                             mk2(__uint_as_float(u[q]), __uint_as_float(v[q])));
+                        const f32x2 y = fma2(x, mk2(s.x, s.x), mk2(s.y, s.y));
                         f32x2 e = mk2(ex2(lo2(y)), ex2(hi2(y)));
                         if (!decltype(all)::value) {
                             const int vq = seen[32 * q4 + q];
@@ -761,22 +862,23 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         }
     } else if (warp == 8) {
         if (lane == 0) {
-            constexpr uint32_t id = f16_idesc(CH_M, CH_M);
-            for (int i = i0, k = 0; i < i1; ++i, ++k) {
-                const int st = k & 1;  // of the query tiles, and the group whose turn it is
-                if (!mbar_wait_bounded(q_full + 8 * st, (k >> 1) & 1, p.err)) break;
-                if (!mbar_wait_bounded(s_free + 8 * st, ((k >> 1) & 1) ^ 1, p.err)) break;
+            constexpr uint32_t id = f16_idesc(CH_M, CW_ROWS);
+            for (int k = 0; k < 2 * (i1 - i0); ++k) {  // half tiles, the groups in turn
+                const int g2 = k & 1, st = k % CW_STAGES;
+                if (!mbar_wait_bounded(q_full + 8 * st, (uint32_t)(k / CW_STAGES) & 1, p.err)) break;
+                if (!mbar_wait_bounded(s_free + 8 * g2, ((k >> 1) & 1) ^ 1, p.err)) break;
                 tc_fence_after();
                 for (int t = 0; t < nact; ++t)
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < 3; ++part)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            tc_mma_f16_ss(tmem + (2 * st + t) * CH_M, sw128_desc(sK + t * S::KT + kk / 4 * CH_SLAB) + 2 * (kk % 4),
-                                          sw128_desc(sQ + st * S::QT + (part * (D / 64) + kk / 4) * CH_SLAB) + 2 * (kk % 4), id,
-                                          (part | kk) != 0);
+                            tc_mma_f16_ss(tmem + (2 * g2 + t) * CH_M + (part > 0 ? CW_ROWS : 0),
+                                          sw128_desc(sK + t * S::KT + kk / 4 * CH_SLAB) + 2 * (kk % 4),
+                                          sw128_desc(sQ + st * S::QT + (part * (D / 64) + kk / 4) * S::SLAB) + 2 * (kk % 4), id,
+                                          part == 2 || kk != 0);
                 tc_commit(q_empty + 8 * st);
-                tc_commit(s_full + 8 * st);
+                tc_commit(s_full + 8 * g2);
             }
             tc_commit(drain);
             mbar_wait_bounded(drain, 0, p.err);
@@ -785,16 +887,17 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     } else if (warp == 9) {
         if (lane == 0) {
             int issued = 0;
-            for (int i = i0, k = 0; i < i1; ++i, ++k) {
-                const int st = k & 1;
-                if (!mbar_wait_bounded(q_empty + 8 * st, ((k >> 1) & 1) ^ 1, p.err)) break;
-                const uint8_t *src = c.tiles + (qslot + i) * S::QT;
+            for (int k = 0; k < 2 * (i1 - i0); ++k) {
+                const int st = k % CW_STAGES;
+                if (!mbar_wait_bounded(q_empty + 8 * st, ((uint32_t)(k / CW_STAGES) & 1) ^ 1, p.err)) break;
+                const uint8_t *src = c.tiles + (qslot + i0 + (k >> 1)) * 2 * S::QT + (k & 1) * S::SLAB;
                 mbar_expect_tx(q_full + 8 * st, S::QT);
-                for (uint32_t o = 0; o < S::QT; o += CH_SLAB) bulk_g2s(sQ + st * S::QT + o, src + o, CH_SLAB, q_full + 8 * st);
+                for (int o = 0; o < 3 * (D / 64); ++o)
+                    bulk_g2s(sQ + st * S::QT + o * S::SLAB, src + o * CH_SLAB, S::SLAB, q_full + 8 * st);
                 issued = k + 1;
             }
-            for (int k = max(0, issued - 2); k < issued; ++k)  // no copy may be in flight when the CTA ends
-                mbar_wait_bounded(q_full + 8 * (k & 1), (k >> 1) & 1, p.err);
+            for (int k = max(0, issued - CW_STAGES); k < issued; ++k)  // no copy may be in flight when the CTA ends
+                mbar_wait_bounded(q_full + 8 * (k % CW_STAGES), (uint32_t)(k / CW_STAGES) & 1, p.err);
         }
         __syncwarp();
     }
@@ -817,7 +920,7 @@ ChunkPlan chunk_plan(int64_t T, int Hq, int H, int D, int dtype, int B, int max_
 {
     ChunkPlan pl;
     const int64_t G = Hq / H, R = T * Hq;
-    pl.qp = weights || dtype == RPTQ_F32 ? 2 : 1;
+    pl.qp = weights || dtype == RPTQ_F32 ? 3 : 1;
     pl.slots = T * G / CH_M + B;
     pl.slots2 = T * G / (2 * CH_M) + B;
     // the positions are split where the blocks of 256 rows leave SMs without one, each part at least four tiles
@@ -846,7 +949,7 @@ cudaError_t launch_chunk(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles,
     if (e != cudaSuccess) return e;
     if (pl.splits > 1 && (e = launch_paged_combine(c.a, D, stream)) != cudaSuccess) return e;
     if (c.a.weights != nullptr) {
-        if constexpr (QP == 2) {
+        if constexpr (QP == 3) {
             if ((e = kernel_smem((const void *)paged_chunk_weights<BITS, D>, WeightShape<D>::SMEM)) != cudaSuccess) return e;
             const int blocks = (c.a.p.max_len + CW_TILES * CH_KEYS - 1) / (CW_TILES * CH_KEYS);
             paged_chunk_weights<BITS, D>
@@ -858,8 +961,8 @@ cudaError_t launch_chunk(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles,
 template <int BITS, int D>
 cudaError_t launch_chunk_prec(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles, int B, cudaStream_t stream)
 {
-    if (c.a.dtype == RPTQ_F32) return launch_chunk<BITS, D, 2, 2>(c, pl, tiles, B, stream);
-    if (pl.qp == 2) return launch_chunk<BITS, D, 2, 1>(c, pl, tiles, B, stream);
+    if (c.a.dtype == RPTQ_F32) return launch_chunk<BITS, D, 3, 2>(c, pl, tiles, B, stream);
+    if (pl.qp == 3) return launch_chunk<BITS, D, 3, 1>(c, pl, tiles, B, stream);
     return launch_chunk<BITS, D, 1, 1>(c, pl, tiles, B, stream);
 }
 }  // namespace
@@ -878,7 +981,7 @@ cudaError_t launch_paged_chunk(const PagedAttnArgs &a)
     d.p = Paged{a.start, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, a.max_q, a.max_len, a.err};
     d.q = a.q, d.out = a.out, d.dtype = a.dtype, d.Hq = a.Hq, d.H = a.H, d.G = a.Hq / a.H, d.q_stride = a.q_stride;
     d.kq = a.kq, d.vq = a.vq, d.kt = a.kt, d.scale = a.scale, d.weights = a.weights, d.splits = pl.splits;
-    d.mid = (float)(1 << (a.bits - 1));
+    d.centred = (1 << a.bits) - 1;
     if (a.weights) d.stat = reinterpret_cast<float *>(ws + pl.stat);
     if (pl.splits > 1) {
         d.part = reinterpret_cast<float *>(ws + pl.part);

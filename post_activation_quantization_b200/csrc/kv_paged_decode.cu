@@ -52,16 +52,7 @@ __device__ __forceinline__ uint32_t mat_trans(uint32_t v)
 // x[i] holds code i of row a in the low half and of row b in the high half, both at bit pos(i).
 template <int BITS, int D>
 struct VCodes {
-    static constexpr int N = D / 8, NW = (N * BITS + 31) / 32, MID = 1 << (BITS - 1);
-    // the codes about their middle, so that the sums over positions stay small where the values cancel
-    template <int I = 0>
-    __device__ __forceinline__ static void about_mid(uint32_t (&x)[N])
-    {
-        if constexpr (I < N) {
-            x[I] = code_about_mid<pos(I), pos(I), MID>(x[I]);
-            about_mid<I + 1>(x);
-        }
-    }
+    static constexpr int N = D / 8, NW = (N * BITS + 31) / 32;
     __host__ __device__ static constexpr int pos(int i)
     {
         if (BITS == 4) return 4 * (i & 1);
@@ -128,12 +119,14 @@ struct VCodes {
 // RT rows to a column tile of 8.  PREC says what the result must be good to:
 //   0 (bf16): q' one fp16, the codes as they are.  A product with a subnormal keeps 10 bits less in the tensor
 //     core's sum (6e-5 of it), which is nothing in bf16.
-//   1 (fp16, or running sums kept): q' in PARTS parts of 11 bits on one fixed grid -- with the codes multiplied up to
+//   1 (fp16, or running sums kept): q' in parts of 11 bits on one fixed grid -- with the codes multiplied up to
 //     normal fp16 numbers every product and every sum of a part is exact -- so that a score has fp32's rounding and no
 //     other; the weights one fp16.
 //   2 (fp32): the same, V's codes multiplied up too and the weights in two fp16 parts.
+// The grid's unit hangs on the row's largest |q'|: two parts, 22 bits of that, do for fp16 outputs; fp32 ones and the
+// sums have three (a few large channels cost the others too much: 2e-5 of the output measured with two, 3e-7 with three).
 // Columns: RT = 1: row 0's part t in column 2t, the odd ones empty (a lane then has half the softmax to do);
-// RT = 4: part * 4 + row; RT = 8 (one part): the rows.
+// RT = 2, 4: part * RT + row; RT = 8 (one part): the rows.
 template <int BITS, int D, int RT, int NT, int PREC>
 struct DecShape {
     static constexpr int ROWS = NT * RT;
@@ -141,28 +134,29 @@ struct DecShape {
     static constexpr int RB = D * BITS / 8;    // bytes of a packed row
     static constexpr uint32_t TILE = DEC_TILE * RB, STAGE = 2 * TILE;
     static constexpr size_t RING = (size_t)DEC_WARPS * DEC_STAGES * STAGE;
-    static constexpr size_t JOIN = (size_t)DEC_WARPS * ROWS * (D + 2) * 4;  // the warps' results, when they are joined
+    static constexpr size_t JOIN = (size_t)DEC_WARPS * ROWS * (D + 3) * 4;  // the warps' results, when they are joined
     static constexpr size_t SMEM = RING > JOIN ? RING : JOIN;
-    static constexpr int PARTS = PREC == 0 ? 1 : RT == 1 ? 3 : 2;  // of q'
+    static constexpr int PARTS = PREC == 0 ? 1 : RT <= 2 ? 3 : 2;  // of q'
     // row in the tile, and part, of column `col`
-    __device__ __forceinline__ static int row(int col) { return RT == 1 ? 0 : RT == 4 ? col & 3 : col; }
-    __device__ __forceinline__ static int part(int col) { return RT == 1 ? col >> 1 : RT == 4 ? col >> 2 : 0; }
-    __device__ __forceinline__ static bool used(int col) { return RT != 1 || ((col & 1) == 0 && (col >> 1) < PARTS); }
+    __device__ __forceinline__ static int row(int col) { return RT == 1 ? 0 : col & (RT - 1); }
+    __device__ __forceinline__ static int part(int col) { return RT <= 2 ? col >> 1 : RT == 4 ? col >> 2 : 0; }
+    __device__ __forceinline__ static bool used(int col) { return part(col) < PARTS && (RT != 1 || (col & 1) == 0); }
 };
 
 template <int BITS, int D, int RT, int NT, int PREC>
-__global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ? 3 : 2)
+__global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CTAS_SM) : NT == 2 && PREC < 2 ? 3 : 2)
     paged_decode_kernel(const PagedAttnDev a)
 {
     using S = DecShape<BITS, D, RT, NT, PREC>;
     using KP = KPairs<BITS, D>;
     using VC = VCodes<BITS, D>;
     constexpr int E = S::E;
-    constexpr int XOR = RT == 1 ? 1 : 2;  // lane distance of a row's two parts
+    constexpr int XOR = RT <= 2 ? 1 : 2;  // lane distance of a row's first two parts
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[DEC_WARPS * DEC_STAGES];
     constexpr int QP = D + 16;  // q' of a row: its quarters 4 floats further apart (their lanes read at once)
     __shared__ float s_sv[D], s_zv[D];
+    __shared__ int s_zc[D];
     // q' and the query fragments (as each lane of a warp holds them).  With one column tile, where four CTAs share an SM,
     // they lie in the last stages of the warps' rings, which no copy uses before the first turn.
     constexpr bool IN_RING = NT == 1;
@@ -178,7 +172,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
         return IN_RING ? reinterpret_cast<uint32_t *>(spare(i / FR)) + i % FR * 32 : s_qf + (nt * KP::N + i) * 32;
     };
     __shared__ __align__(16) uint8_t s_ref[S::RB];
-    __shared__ float s_fac[S::ROWS][32], s_max[S::ROWS], s_inv[S::ROWS];
+    __shared__ float s_fac[S::ROWS][32], s_max[S::ROWS], s_inv[S::ROWS], s_winv[S::ROWS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
     const Paged &p = a.p;
     const int split = blockIdx.x % a.splits;
@@ -242,7 +236,9 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
             q[r] = r < rows ? load_elem(a.q, a.dtype, (int64_t)(s0 + tok) * a.q_stride + (int64_t)(h * a.G + j) * D + tid) : 0.f;
         }
         s_sv[tid] = a.kt.sv[cv];
-        s_zv[tid] = (float)a.kt.zv[cv] - (PREC == 2 ? VC::MID : 0);
+        const int zv = a.kt.zv[cv], zc = PREC == 2 ? zero_code(zv, (1 << BITS) - 1) : 0;
+        s_zv[tid] = (float)(zv - zc);
+        s_zc[tid] = zc;
 #pragma unroll
         for (int r = 0; r < S::ROWS; ++r) q_row(r)[tid + tid / (D / 4) * 4] = q[r] * sk;
     }
@@ -329,18 +325,29 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
 
     float o[D / 16][NT][4];  // sums over the warp's positions: channels 2i, 2i + 1 of the lane's D / 8, two columns
     float m[NT][E], off[NT][E], l[NT][E];  // reference of the exponents, DEC_PSHIFT - m, sum
+    // Outputs are divided by the sum of the weights as rounded for their product, running sums by the weights' own
+    constexpr bool OWN = PREC == 1 && RT <= 2;
+    float lw[NT][E];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             m[nt][e] = -1e30f;
             off[nt][e] = vis[nt][e] > 0 ? 1e30f : -INFINITY;
-            l[nt][e] = 0.f;
+            l[nt][e] = lw[nt][e] = 0.f;
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
+    }
+    uint32_t vc[PREC == 2 ? VC::N : 1];  // what is taken off V's codes
+    if constexpr (PREC == 2) {
+#pragma unroll
+        for (int j = 0; j < VC::N; ++j) {
+            const float c = code_offset(s_zc[gq * (D / 8) + j], VC::pos(j));
+            vc[j] = half2_bits(c, c);
+        }
     }
     // position of MMA row k (0-15) of a block: k with its low bits arranged so that the rows that the lanes of one
     // shared-memory access read are neighbours, for K (rows gq) and for V (k = 2 tq, ...) alike
@@ -384,7 +391,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
                             float &v = x[bk][nt][2 * f + e];
                             v *= part_scale;
                             v += __shfl_xor_sync(FULL, v, XOR);
-                            if (RT == 1) v += __shfl_xor_sync(FULL, v, 2);
+                            if (RT <= 2) v += __shfl_xor_sync(FULL, v, 2);
                         }
                 }
             }
@@ -453,10 +460,12 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
 #pragma unroll
                     for (int f = 4; f < 32; f <<= 1) mn = fmaxf(mn, __shfl_xor_sync(FULL, mn, f));
                     if (vis[nt][e] > 0 && mn > -1e30f) {
+                        mn = ceilf(mn);  // an integer: DEC_PSHIFT - m is exact, and so is the factor between two references
                         const float r = ex2(m[nt][e] - mn);
                         m[nt][e] = mn;
                         off[nt][e] = (float)DEC_PSHIFT - mn;
                         l[nt][e] *= r;
+                        lw[nt][e] *= r;
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) {
                             o[c][nt][e] *= r;
@@ -491,6 +500,10 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
                     } else {  // the rounded weights are summed: numerator and denominator hold the same ones
                         l[nt][0] += r2.x;
                         if (E == 2) l[nt][E - 1] += r2.y;
+                        if (OWN) {
+#pragma unroll
+                            for (int e = 0; e < E; ++e) lw[nt][e] += pv[e];
+                        }
                     }
                     w[nt][f] = mat_trans(hw);
                 }
@@ -502,14 +515,24 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
             VC::load(vst + (16 * bk + v1 + 8) * S::RB, gq, rc);
             VC::join(ra, rc, xb);
             if constexpr (PREC == 2) {
-                VC::about_mid(xa);
-                VC::about_mid(xb);
+#pragma unroll
+                for (int j = 0; j < VC::N; ++j) xa[j] = code_up_plus(xa[j], vc[j]), xb[j] = code_up_plus(xb[j], vc[j]);
             }
 #pragma unroll
             for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_16816(o[c][nt], xa[2 * c], xa[2 * c + 1], xb[2 * c], xb[2 * c + 1], w[nt][0], w[nt][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (PREC == 2) {
+                        // The tensor core cuts its sums off at the accumulator's last bit, every one to the same side (1.3e-6
+                        // of the result after 8540 positions, measured): over the blocks they are added and rounded here.
+                        float t[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_16816(t, xa[2 * c], xa[2 * c + 1], xb[2 * c], xb[2 * c + 1], w[nt][0], w[nt][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[c][nt][e] += t[e];
+                    } else {
+                        mma_16816(o[c][nt], xa[2 * c], xa[2 * c + 1], xb[2 * c], xb[2 * c + 1], w[nt][0], w[nt][1]);
+                    }
+                }
         }
         __syncwarp();  // the stage has been read (its values went into the MMAs above)
     }
@@ -523,11 +546,14 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
-            for (int f = 4; f < 32; f <<= 1) l[nt][e] += __shfl_xor_sync(FULL, l[nt][e], f);
+            for (int f = 4; f < 32; f <<= 1) {
+                l[nt][e] += __shfl_xor_sync(FULL, l[nt][e], f);
+                if (OWN) lw[nt][e] += __shfl_xor_sync(FULL, lw[nt][e], f);
+            }
     __syncthreads();  // every warp is done with its ring
     float *js = reinterpret_cast<float *>(smem);            // [warp][row][D]
     float *jm = js + DEC_WARPS * S::ROWS * D;               // [warp][row]
-    float *jl = jm + DEC_WARPS * S::ROWS;
+    float *jl = jm + DEC_WARPS * S::ROWS, *jw = jl + DEC_WARPS * S::ROWS;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -546,6 +572,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
             if (gq == 0 && head) {
                 jm[warp * S::ROWS + r] = l[nt][e] == 0.f ? -INFINITY : m[nt][e];
                 jl[warp * S::ROWS + r] = l[nt][e] * (1.f / (float)(1 << DEC_PSHIFT));
+                jw[warp * S::ROWS + r] = (OWN ? lw[nt][e] : l[nt][e]) * (1.f / (float)(1 << DEC_PSHIFT));
             }
         }
     __syncthreads();
@@ -580,15 +607,23 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
     cluster.sync();
     for (int r = warp; r < rows; r += DEC_WARPS) {
         const float *om = cluster.map_shared_rank(jm, min(lane / DEC_WARPS, a.splits - 1));
-        const float *ol = om + (jl - jm);
+        const float *ol = om + (jl - jm), *ow = om + (jw - jm);
         const float mw = lane < all ? om[lane % DEC_WARPS * S::ROWS + r] : -INFINITY;
         float mt = mw;
         for (int f = 16; f > 0; f >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, f));
         const float f = mw == -INFINITY ? 0.f : ex2(mw - mt);
         float lt = lane < all ? ol[lane % DEC_WARPS * S::ROWS + r] * f : 0.f;
-        for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(FULL, lt, o);
+        float wt = OWN && lane < all ? ow[lane % DEC_WARPS * S::ROWS + r] * f : 0.f;
+        for (int o = 16; o > 0; o >>= 1) {
+            lt += __shfl_xor_sync(FULL, lt, o);
+            if (OWN) wt += __shfl_xor_sync(FULL, wt, o);
+        }
         s_fac[r][lane] = f;
-        if (lane == 0) s_max[r] = mt, s_inv[r] = mt == -INFINITY ? 0.f : 1.f / lt;
+        if (lane == 0) {
+            s_max[r] = mt;
+            s_inv[r] = mt == -INFINITY ? 0.f : 1.f / lt;
+            s_winv[r] = mt == -INFINITY ? 0.f : 1.f / (OWN ? wt : lt);
+        }
     }
     __syncthreads();
     for (int i = split * DEC_THREADS + tid; i < rows * D; i += a.splits * DEC_THREADS) {
@@ -620,7 +655,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? DEC_CTAS_SM : NT == 2 ?
                 const int seen = L - n + r / a.G + 1;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (at[u] && pos[u] < seen) w[u] = fmaf(ex2(x[pos[u]] - s_max[r]), s_inv[r], w[u]);
+                    if (at[u] && pos[u] < seen) w[u] = fmaf(ex2(x[pos[u]] - s_max[r]), s_winv[r], w[u]);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -667,7 +702,7 @@ __global__ void __launch_bounds__(CMB_THREADS)
 #pragma unroll 8
         for (int s = 0; s < a.splits; ++s) v = fmaf(a.part[(s * R + row) * D + d], s_f[s], v);
         const int k = cluster_of(a.kt.cv, h * D + d, a.kt.g, p.err);
-        store_elem(a.out, a.dtype, row * D + d, mt == -INFINITY ? 0.f : a.kt.sv[k] * (v - ((float)a.kt.zv[k] - a.mid)));
+        store_elem(a.out, a.dtype, row * D + d, mt == -INFINITY ? 0.f : a.kt.sv[k] * (v - (float)(a.kt.zv[k] - zero_code(a.kt.zv[k], a.centred))));
     }
 }
 
@@ -683,7 +718,7 @@ DecPlan dec_plan(int Hq, int H, int dtype, int B, int max_q, int max_len, int we
     DecPlan pl;
     const int64_t rows = (int64_t)max_q * (Hq / H);
     pl.prec = dtype == RPTQ_F32 ? 2 : weights || dtype == RPTQ_F16 ? 1 : 0;
-    pl.rt = rows == 1 ? 1 : pl.prec ? 4 : 8;
+    pl.rt = rows == 1 ? 1 : weights || pl.prec == 2 ? 2 : pl.prec == 1 ? 4 : 8;
     pl.nt = rows <= pl.rt ? 1 : rows <= 2 * pl.rt ? 2 : 4;
     // Parts: about DEC_CTAS_SM CTAs to an SM in all, each warp at least a tile.  Up to DEC_CLUSTER (always, where running sums are kept)
     // they are a cluster, which joins itself; more leave their results to a second kernel.
@@ -700,12 +735,12 @@ DecPlan dec_plan(int Hq, int H, int dtype, int B, int max_q, int max_len, int we
 }
 }  // namespace
 
-// at most 16 rows in two parts, 32 in one
+// at most four column tiles: 8 rows in three parts, 16 in two, 32 in one
 bool paged_decode_takes(int Hq, int H, int D, int dtype, int max_q, int weights)
 {
     if (D != 64 && D != 128) return false;
     const int64_t rows = (int64_t)max_q * (Hq / H);
-    return rows <= (weights || dtype != RPTQ_BF16 ? 16 : 32);
+    return rows <= (weights || dtype == RPTQ_F32 ? 8 : dtype == RPTQ_F16 ? 16 : 32);
 }
 
 size_t paged_decode_workspace(int64_t T, int Hq, int H, int D, int dtype, int B, int max_q, int max_len, int weights,
@@ -754,11 +789,9 @@ static cudaError_t launch_dec_prec(const PagedAttnDev &d, const DecPlan &pl, int
 template <int BITS, int D>
 static cudaError_t launch_dec_rows(const PagedAttnDev &d, const DecPlan &pl, int B, cudaStream_t stream)
 {
-    switch (pl.prec) {
-    case 2: return launch_dec_prec<BITS, D, 4, 2>(d, pl, B, stream);
-    case 1: return launch_dec_prec<BITS, D, 4, 1>(d, pl, B, stream);
-    default: return launch_dec_prec<BITS, D, 8, 0>(d, pl, B, stream);
-    }
+    if (pl.prec == 2) return launch_dec_prec<BITS, D, 2, 2>(d, pl, B, stream);
+    if (pl.prec == 0) return launch_dec_prec<BITS, D, 8, 0>(d, pl, B, stream);
+    return d.weights ? launch_dec_prec<BITS, D, 2, 1>(d, pl, B, stream) : launch_dec_prec<BITS, D, 4, 1>(d, pl, B, stream);
 }
 
 cudaError_t launch_paged_decode(const PagedAttnArgs &a)
@@ -768,7 +801,7 @@ cudaError_t launch_paged_decode(const PagedAttnArgs &a)
     d.p = Paged{a.start, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, a.max_q, a.max_len, a.err};
     d.q = a.q, d.out = a.out, d.dtype = a.dtype, d.Hq = a.Hq, d.H = a.H, d.G = a.Hq / a.H, d.q_stride = a.q_stride;
     d.kq = a.kq, d.vq = a.vq, d.kt = a.kt, d.scale = a.scale, d.weights = a.weights, d.splits = pl.splits;
-    d.mid = pl.prec == 2 ? (float)(1 << (a.bits - 1)) : 0.f;
+    d.centred = pl.prec == 2 ? (1 << a.bits) - 1 : 0;
     if (a.weights) d.scores = static_cast<float *>(a.ws);
     if (pl.second) {
         d.part = static_cast<float *>(a.ws);
