@@ -13,10 +13,10 @@
 // scores of a row, which the softmax does not see; S then has the size of the scores' spread), V's relative to the code
 // nearest to the channel's zero point.
 // Queries come from a first kernel as finished operand tiles, already scaled (q' = q s) and in the 128-byte swizzle.
-// Where the scores must be good to fp32 (fp32 queries, or running sums of weights), q' has three parts and S takes three
-// products, in two accumulators of 64 positions.  fp32 outputs have W in two parts as well, and the products of a tile are
-// added to O by the softmax's threads: the tensor core's own additions are cut off at the accumulator's last bit, and the
-// many of a long row would all err to the same side (4e-6 after 1287 positions, measured).
+// Where the scores must be good to fp32 (fp32 queries, or running sums of weights), q' has two fp16 parts and S takes two
+// products.  fp32 outputs have W in two parts as well, tiles of 64 positions, and the products of a tile are added to O by
+// the softmax's threads: the tensor core's own additions are cut off at the accumulator's last bit, and the many of a long
+// row would all err to the same side (4e-6 after 1287 positions, measured).
 //
 // Running sums: a third kernel goes over the positions again with the rows' maxima and sums known: tiles of 128
 // positions are the row operand, S^T = K q'^T, so that a thread owns a position and adds its weights in registers,
@@ -133,8 +133,9 @@ __device__ __forceinline__ void load_row(const void *p, int dtype, int64_t at, f
 
 // ---- the queries as operand tiles -----------------------------------------------------------------------
 // One CTA per (tile slot, head), a warp to a row.  PARTS = 1: fp16 of q' scaled so that the row's largest is in
-// [2^14, 2^15).  3: integers of 11 bits on grids of 2^-11 of each other, relative to the row's largest; the second is
-// stored as an integer (it has an accumulator of its own), the third in the second's unit.
+// [2^14, 2^15); 2: and what that rounding leaves, as fp16 too: 22 bits of every element.  (Two integers on one grid
+// relative to the row's largest would keep the sums of the first part exact, but a row with an outlier then leaves its
+// other channels few bits: 3.6e-6 of the running sums instead of 2e-8, measured.)
 constexpr int CQ_THREADS = 256;
 template <int BITS, int D, int PARTS>
 __global__ void __launch_bounds__(CQ_THREADS)
@@ -196,22 +197,17 @@ __global__ void __launch_bounds__(CQ_THREADS)
             int ex = 0;
             if (m[u] > 0.f && m[u] < INFINITY) frexpf(m[u], &ex);
             ex = max(ex, -100);
-            const int grid = PARTS == 1 ? 15 : 11;
-            const float up = __uint_as_float((uint32_t)(127 + grid - ex) << 23);  // 2^(grid - ex): grid - ex <= 115
-            if (lane == 0) c.cx[((int64_t)h * c.slots + slot) * CH_M + r] = ldexpf(a.scale * LOG2E, ex - grid + 10);
+            const float up = __uint_as_float((uint32_t)(127 + 15 - ex) << 23);  // 2^(15 - ex): 15 - ex <= 115
+            if (lane == 0) c.cx[((int64_t)h * c.slots + slot) * CH_M + r] = ldexpf(a.scale * LOG2E, ex - 15 + 10);
 #pragma unroll
             for (int k = 0; k < CPL; ++k) {
                 const uint32_t sw = (s_at[lane * CPL + k] + r * 128) ^ ((r & 7) << 4);  // piece c of a row sits at c ^ (row mod 8)
                 const float down = s_down[lane * CPL + k];
                 float f = v[u][k] * up;
-                const float g = PARTS == 1 ? f : rintf(f);
-                *reinterpret_cast<__half *>(tile + sw) = __float2half_rn(g * down);
-                if (PARTS > 1) {  // (every difference and product is exact)
-                    f = (f - g) * 2048.f;
-                    const float g2 = rintf(f), g3 = rintf((f - g2) * 2048.f) * 0x1p-11f;
-                    *reinterpret_cast<__half *>(tile + (D / 64) * CH_SLAB + sw) = __float2half_rn(g2 * down);
-                    *reinterpret_cast<__half *>(tile + 2 * (D / 64) * CH_SLAB + sw) = __float2half_rn(g3 * down);
-                }
+                f *= down;
+                const __half hi = __float2half_rn(f);
+                *reinterpret_cast<__half *>(tile + sw) = hi;
+                if (PARTS == 2) *reinterpret_cast<__half *>(tile + (D / 64) * CH_SLAB + sw) = __float2half_rn(f - __half2float(hi));
             }
         }
     }
@@ -306,15 +302,13 @@ __device__ __forceinline__ void chunk_reference(const PagedAttnDev &a, int b, in
 }
 
 // ---- attention --------------------------------------------------------------------------------------------
-template <int D, int QP>  // QP: parts of q', 1 or 3
+template <int D, int QP, int PP>  // parts of q' and of W
 struct ChunkShape {
     static constexpr int SLABS = D / 64;
-    // Positions of a tile.  With more than one part, S has two accumulators (the sums of the first part, and those of the
-    // others, are exact or nearly so by themselves; in one they would lose what is below 2^-24 of the larger): half as many.
-    static constexpr int KEYS = QP == 1 ? 128 : 64;
+    static constexpr int KEYS = PP == 2 ? 64 : 128;  // positions of a tile
     static constexpr uint32_t KV_SLAB = KEYS * 128, KV = SLABS * KV_SLAB;  // a K or V tile
     static constexpr uint32_t QT = QP * SLABS * CH_SLAB;                   // a query tile
-    static constexpr int STAGES = QP == 3 && D == 128 ? 1 : 2;             // what 227 KB leave
+    static constexpr int STAGES = QP == 2 && PP == 1 && D == 128 ? 1 : 2;  // what 227 KB leave
     static constexpr uint32_t SMEM = 1024 + 2 * QT + 2 * STAGES * KV;
     static constexpr uint32_t O_COL = 256;  // O of tile g at O_COL + g * D
 };
@@ -323,11 +317,11 @@ template <int BITS, int D, int QP, int PP>
 __global__ void __launch_bounds__(CH_THREADS, 1)
     paged_chunk_kernel(const ChunkDev c)
 {
-    using S = ChunkShape<D, QP>;
+    using S = ChunkShape<D, QP, PP>;
     using KP = KPairs<BITS, D>;
     constexpr int ST = S::STAGES, KEYS = S::KEYS;
-    constexpr float SHIFT = QP == 3 && PP == 1 ? 0.f : CH_PSHIFT;  // of the weights' exponents (see CH_PSHIFT)
-    constexpr int HALVES = D / 64;  // PP = 2: a tile's product, 64 channels at a time, lies where S's second accumulator was
+    constexpr float SHIFT = QP == 2 && PP == 1 ? 0.f : CH_PSHIFT;  // of the weights' exponents (see CH_PSHIFT)
+    constexpr int HALVES = D / 64;  // PP = 2: a tile's product, 64 channels at a time, lies beside S
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[4 * 2 + 4 * 2 + 2];
     __shared__ uint32_t tmem_slot;
@@ -411,17 +405,12 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 const int pos0 = j * KEYS;
                 const bool whole = pos0 + KEYS <= vmin;
                 float top = -INFINITY;
-                uint32_t v[4][32];  // the row of S
+                uint32_t v[KEYS / 32][32];  // the row of S
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) tc_ld32_async(tS + 32 * q4, v[q4]);
+                for (int q4 = 0; q4 < KEYS / 32; ++q4) tc_ld32_async(tS + 32 * q4, v[q4]);
                 tc_wait_ld();
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) tc_loaded(v[q4]);
-                if (QP > 1) {  // the first part's sums and the others'
-#pragma unroll
-                    for (int k = 0; k < KEYS; ++k)
-                        v[k / 32][k % 32] = __float_as_uint(fmaf(__uint_as_float(v[2 + k / 32][k % 32]), 0x1p-11f, __uint_as_float(v[k / 32][k % 32])));
-                }
+                for (int q4 = 0; q4 < KEYS / 32; ++q4) tc_loaded(v[q4]);
                 if (!whole) {
 #pragma unroll
                     for (int k = 0; k < KEYS; ++k)
@@ -627,9 +616,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 for (int part = 0; part < QP; ++part)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        tc_mma_f16_ss(tmem + (uint32_t)(g * CH_M + (part > 0 ? KEYS : 0)),
+                        tc_mma_f16_ss(tmem + (uint32_t)g * CH_M,
                                       sw128_desc(q0 + (part * S::SLABS + kk / 4) * CH_SLAB) + 2 * (kk % 4),
-                                      sw128_desc(sK + st * S::KV + kk / 4 * S::KV_SLAB) + 2 * (kk % 4), qk, part == 2 || kk != 0);
+                                      sw128_desc(sK + st * S::KV + kk / 4 * S::KV_SLAB) + 2 * (kk % 4), qk, (part | kk) != 0);
                 tc_commit(s_full + 8 * g);
             };
             bool ok = mbar_wait_bounded(q_full, 0, p.err);
@@ -705,17 +694,16 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
 }
 
 // ---- running sums -------------------------------------------------------------------------------------------
-// One CTA per (sequence, head, 256 positions), all 512 tensor-memory columns: S^T of two tiles of 128 positions and half a
-// row tile, in two accumulators, twice.  Warps 0-3 take the first half of each row tile and warps 4-7 the second; a thread
+// One CTA per (sequence, head, 256 positions), all 512 tensor-memory columns: S^T of two tiles of 128 positions and a row
+// tile, twice.  Warps 0-3 and 4-7 take the row tiles in turn; a thread
 // has one position of each tile, so that what it reads of a row from shared memory (8 bytes for every lane: two clocks of the
 // 128 bytes a clock) serves two weights.  Warp 8 issues the
-// MMAs, warp 9 the copies of the query half tiles (three in flight).
-constexpr int CW_THREADS = 320, CW_TILES = 2, CW_ROWS = CH_M / 2, CW_STAGES = 3;
+// MMAs, warp 9 the copies of the query tiles (two in flight).
+constexpr int CW_THREADS = 320, CW_TILES = 2;
 template <int D>
 struct WeightShape {
-    static constexpr uint32_t SLAB = CW_ROWS * 128, QT = 3 * (D / 64) * SLAB;  // of half a row tile
-    static constexpr uint32_t KT = (D / 64) * CH_SLAB;
-    static constexpr uint32_t SMEM = 1024 + CW_STAGES * QT + CW_TILES * KT;
+    static constexpr uint32_t QT = 2 * (D / 64) * CH_SLAB, KT = (D / 64) * CH_SLAB;
+    static constexpr uint32_t SMEM = 1024 + 2 * QT + CW_TILES * KT;
 };
 template <int BITS, int D>
 __global__ void __launch_bounds__(CW_THREADS, 1)
@@ -724,10 +712,10 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     using S = WeightShape<D>;
     using KP = KPairs<BITS, D>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * CW_STAGES + 5];
+    __shared__ __align__(8) uint64_t bars[9];
     __shared__ uint32_t tmem_slot;
-    __shared__ __align__(16) float2 s_row[2][2][CW_ROWS];  // [group][turn][row]: cx, -(maximum + log2 of the sum)
-    __shared__ int s_vis[2][2][CW_ROWS];                 // visible positions
+    __shared__ __align__(16) float2 s_row[2][2][CH_M];  // [group][turn][row]: cx, -(maximum + log2 of the sum)
+    __shared__ int s_vis[2][2][CH_M];                   // visible positions
     __shared__ float2 s_sum[CH_M];
     const PagedAttnDev &a = c.a;
     const Paged &p = a.p;
@@ -741,15 +729,13 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     const int64_t qslot = (int64_t)h * c.slots + chunk_base(p, b, a.G, CH_M);
     const int i0 = (int)((int64_t)max(0, first - (L - n)) * a.G / CH_M), i1 = (R + CH_M - 1) / CH_M;  // row tiles that see the block
 
-    const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u, sK = sQ + CW_STAGES * S::QT;
+    const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u, sK = sQ + 2 * S::QT;
     const uint32_t bar = smem_u32(bars);
-    const uint32_t q_full = bar, q_empty = q_full + 8 * CW_STAGES, s_full = q_empty + 8 * CW_STAGES, s_free = s_full + 16, drain = s_free + 16;
+    const uint32_t q_full = bar, q_empty = bar + 16, s_full = bar + 32, s_free = bar + 48, drain = bar + 64;
     if (tid == 0) {
-        for (int i = 0; i < CW_STAGES; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 1);
             mbar_init(q_empty + 8 * i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 1);
             mbar_init(s_free + 8 * i, CH_M);
         }
@@ -781,32 +767,30 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
 
     if (warp < 8) {
         const int quad = warp & 3, r = 32 * quad + lane;
-        const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)g * CW_TILES * CH_M;  // tile, part, row
+        const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)g * CW_TILES * CH_M;
         const int pos = first + r;  // and pos + 128
-        // the row of tile i that the thread (of the group's first 64) fetches
+        // the thread's row of tile i
         auto info = [&](int i, float2 &f, int &vis) {
-            const int row = i * CH_M + g * CW_ROWS + r;
+            const int row = i * CH_M + r;
             f = make_float2(0.f, -INFINITY);
             vis = 0;
-            if (i >= i1 || r >= CW_ROWS || row >= R) return;
+            if (i >= i1 || row >= R) return;
             const int tok = row / a.G, j = row - tok * a.G;
             const float2 st = *reinterpret_cast<const float2 *>(a.stat + 2 * ((int64_t)(s0 + tok) * a.Hq + h * a.G + j));
             // scores are relative to position 0's, so the maximum is small enough for the sum's log to be added to it
-            f = make_float2(c.cx[(qslot + i) * CH_M + g * CW_ROWS + r], st.y > 0.f ? log2f(st.y) - st.x : st.y == 0.f ? -INFINITY : st.y);
+            f = make_float2(c.cx[(qslot + i) * CH_M + r], st.y > 0.f ? log2f(st.y) - st.x : st.y == 0.f ? -INFINITY : st.y);
             vis = L - n + tok + 1;
         };
         f32x2 w = mk2(0.f, 0.f);  // of pos, pos + 128
         bool ok = true;
         float2 f;
         int vis;
-        info(i0, f, vis);
-        for (int i = i0, k = 0; i < i1; ++i, ++k) {  // every warp takes every turn: the barrier counts them
-            if (r < CW_ROWS) {
-                s_row[g][k & 1][r] = f;
-                s_vis[g][k & 1][r] = vis;
-            }
+        info(i0 + g, f, vis);
+        for (int i = i0 + g, k = 0; i < i1; i += 2, ++k) {  // every warp takes every turn: the barrier counts them
+            s_row[g][k & 1][r] = f;
+            s_vis[g][k & 1][r] = vis;
             asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
-            info(i + 1, f, vis);  // in flight during this turn
+            info(i + 2, f, vis);  // in flight during this turn
             ok = ok && __all_sync(FULL, mbar_wait_bounded(s_full + 8 * g, k & 1, p.err));
             if (!ok) continue;
             tc_fence_after();
@@ -815,30 +799,26 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             const int *seen = s_vis[g][k & 1];
             auto add = [&](auto all) {
 #pragma unroll
-                for (int q4 = 0; q4 < CW_ROWS / 32; ++q4) {
-                    uint32_t u[32], v[32], u2[32], v2[32];
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    uint32_t u[32], v[32];
                     tc_ld32_async(tS + 32 * q4, u);
-                    tc_ld32_async(tS + CW_ROWS + 32 * q4, u2);
                     tc_ld32_async(tS + CH_M + 32 * q4, v);  // (of no use, and not used, without a second tile)
-                    tc_ld32_async(tS + CH_M + CW_ROWS + 32 * q4, v2);
                     tc_wait_ld();
                     tc_loaded(u);
-                    tc_loaded(u2);
                     tc_loaded(v);
-                    tc_loaded(v2);
+                    f32x2 t = mk2(0.f, 0.f);  // (32 at a time: the sum of 5384 rows in one chain was off by 1.6e-6)
 #pragma unroll
                     for (int q = 0; q < 32; ++q) {
                         const float2 s = rows[32 * q4 + q];
-                        const f32x2 x = fma2(mk2(__uint_as_float(u2[q]), __uint_as_float(v2[q])), mk2(0x1p-11f, 0x1p-11f),
-                                             mk2(__uint_as_float(u[q]), __uint_as_float(v[q])));
-                        const f32x2 y = fma2(x, mk2(s.x, s.x), mk2(s.y, s.y));
+                        const f32x2 y = fma2(mk2(__uint_as_float(u[q]), __uint_as_float(v[q])), mk2(s.x, s.x), mk2(s.y, s.y));
                         f32x2 e = mk2(ex2(lo2(y)), ex2(hi2(y)));
                         if (!decltype(all)::value) {
                             const int vq = seen[32 * q4 + q];
                             e = mk2(pos < vq ? lo2(e) : 0.f, pos + CH_KEYS < vq ? hi2(e) : 0.f);
                         }
-                        w = add2(w, e);
+                        t = add2(t, e);
                     }
+                    w = add2(w, t);
                 }
             };
             if (whole)
@@ -862,23 +842,22 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         }
     } else if (warp == 8) {
         if (lane == 0) {
-            constexpr uint32_t id = f16_idesc(CH_M, CW_ROWS);
-            for (int k = 0; k < 2 * (i1 - i0); ++k) {  // half tiles, the groups in turn
-                const int g2 = k & 1, st = k % CW_STAGES;
-                if (!mbar_wait_bounded(q_full + 8 * st, (uint32_t)(k / CW_STAGES) & 1, p.err)) break;
-                if (!mbar_wait_bounded(s_free + 8 * g2, ((k >> 1) & 1) ^ 1, p.err)) break;
+            constexpr uint32_t id = f16_idesc(CH_M, CH_M);
+            for (int i = i0, k = 0; i < i1; ++i, ++k) {
+                const int st = k & 1;  // of the query tiles, and the group whose turn it is
+                if (!mbar_wait_bounded(q_full + 8 * st, (k >> 1) & 1, p.err)) break;
+                if (!mbar_wait_bounded(s_free + 8 * st, ((k >> 1) & 1) ^ 1, p.err)) break;
                 tc_fence_after();
                 for (int t = 0; t < nact; ++t)
 #pragma unroll
-                    for (int part = 0; part < 3; ++part)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            tc_mma_f16_ss(tmem + (2 * g2 + t) * CH_M + (part > 0 ? CW_ROWS : 0),
-                                          sw128_desc(sK + t * S::KT + kk / 4 * CH_SLAB) + 2 * (kk % 4),
-                                          sw128_desc(sQ + st * S::QT + (part * (D / 64) + kk / 4) * S::SLAB) + 2 * (kk % 4), id,
-                                          part == 2 || kk != 0);
+                            tc_mma_f16_ss(tmem + (2 * st + t) * CH_M, sw128_desc(sK + t * S::KT + kk / 4 * CH_SLAB) + 2 * (kk % 4),
+                                          sw128_desc(sQ + st * S::QT + (part * (D / 64) + kk / 4) * CH_SLAB) + 2 * (kk % 4), id,
+                                          (part | kk) != 0);
                 tc_commit(q_empty + 8 * st);
-                tc_commit(s_full + 8 * g2);
+                tc_commit(s_full + 8 * st);
             }
             tc_commit(drain);
             mbar_wait_bounded(drain, 0, p.err);
@@ -887,17 +866,16 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     } else if (warp == 9) {
         if (lane == 0) {
             int issued = 0;
-            for (int k = 0; k < 2 * (i1 - i0); ++k) {
-                const int st = k % CW_STAGES;
-                if (!mbar_wait_bounded(q_empty + 8 * st, ((uint32_t)(k / CW_STAGES) & 1) ^ 1, p.err)) break;
-                const uint8_t *src = c.tiles + (qslot + i0 + (k >> 1)) * 2 * S::QT + (k & 1) * S::SLAB;
+            for (int i = i0, k = 0; i < i1; ++i, ++k) {
+                const int st = k & 1;
+                if (!mbar_wait_bounded(q_empty + 8 * st, ((k >> 1) & 1) ^ 1, p.err)) break;
+                const uint8_t *src = c.tiles + (qslot + i) * S::QT;
                 mbar_expect_tx(q_full + 8 * st, S::QT);
-                for (int o = 0; o < 3 * (D / 64); ++o)
-                    bulk_g2s(sQ + st * S::QT + o * S::SLAB, src + o * CH_SLAB, S::SLAB, q_full + 8 * st);
+                for (uint32_t o = 0; o < S::QT; o += CH_SLAB) bulk_g2s(sQ + st * S::QT + o, src + o, CH_SLAB, q_full + 8 * st);
                 issued = k + 1;
             }
-            for (int k = max(0, issued - CW_STAGES); k < issued; ++k)  // no copy may be in flight when the CTA ends
-                mbar_wait_bounded(q_full + 8 * (k % CW_STAGES), (uint32_t)(k / CW_STAGES) & 1, p.err);
+            for (int k = max(0, issued - 2); k < issued; ++k)  // no copy may be in flight when the CTA ends
+                mbar_wait_bounded(q_full + 8 * (k & 1), (k >> 1) & 1, p.err);
         }
         __syncwarp();
     }
@@ -920,7 +898,7 @@ ChunkPlan chunk_plan(int64_t T, int Hq, int H, int D, int dtype, int B, int max_
 {
     ChunkPlan pl;
     const int64_t G = Hq / H, R = T * Hq;
-    pl.qp = weights || dtype == RPTQ_F32 ? 3 : 1;
+    pl.qp = weights || dtype == RPTQ_F32 ? 2 : 1;
     pl.slots = T * G / CH_M + B;
     pl.slots2 = T * G / (2 * CH_M) + B;
     // the positions are split where the blocks of 256 rows leave SMs without one, each part at least four tiles
@@ -940,16 +918,16 @@ cudaError_t launch_chunk(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles,
 {
     constexpr size_t qsmem = (size_t)QP * (D / 64) * CH_SLAB;
     cudaError_t e = kernel_smem((const void *)paged_chunk_queries<BITS, D, QP>, qsmem);
-    if (e == cudaSuccess) e = kernel_smem((const void *)paged_chunk_kernel<BITS, D, QP, PP>, ChunkShape<D, QP>::SMEM);
+    if (e == cudaSuccess) e = kernel_smem((const void *)paged_chunk_kernel<BITS, D, QP, PP>, ChunkShape<D, QP, PP>::SMEM);
     if (e != cudaSuccess) return e;
     paged_chunk_queries<BITS, D, QP><<<(unsigned)(pl.slots * c.a.H), CQ_THREADS, qsmem, stream>>>(c, tiles);
     paged_chunk_kernel<BITS, D, QP, PP>
-        <<<(unsigned)(pl.slots2 * c.a.H * pl.splits), CH_THREADS, ChunkShape<D, QP>::SMEM, stream>>>(c);
+        <<<(unsigned)(pl.slots2 * c.a.H * pl.splits), CH_THREADS, ChunkShape<D, QP, PP>::SMEM, stream>>>(c);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (pl.splits > 1 && (e = launch_paged_combine(c.a, D, stream)) != cudaSuccess) return e;
     if (c.a.weights != nullptr) {
-        if constexpr (QP == 3) {
+        if constexpr (QP == 2) {
             if ((e = kernel_smem((const void *)paged_chunk_weights<BITS, D>, WeightShape<D>::SMEM)) != cudaSuccess) return e;
             const int blocks = (c.a.p.max_len + CW_TILES * CH_KEYS - 1) / (CW_TILES * CH_KEYS);
             paged_chunk_weights<BITS, D>
@@ -961,8 +939,8 @@ cudaError_t launch_chunk(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles,
 template <int BITS, int D>
 cudaError_t launch_chunk_prec(const ChunkDev &c, const ChunkPlan &pl, uint8_t *tiles, int B, cudaStream_t stream)
 {
-    if (c.a.dtype == RPTQ_F32) return launch_chunk<BITS, D, 3, 2>(c, pl, tiles, B, stream);
-    if (pl.qp == 3) return launch_chunk<BITS, D, 3, 1>(c, pl, tiles, B, stream);
+    if (c.a.dtype == RPTQ_F32) return launch_chunk<BITS, D, 2, 2>(c, pl, tiles, B, stream);
+    if (pl.qp == 2) return launch_chunk<BITS, D, 2, 1>(c, pl, tiles, B, stream);
     return launch_chunk<BITS, D, 1, 1>(c, pl, tiles, B, stream);
 }
 }  // namespace
