@@ -6,8 +6,8 @@
 // (kv_paged_attn.cuh), and the query rows are its 8 columns:
 //     S [16 positions, 8 rows] = codes of K [16, D] x q'^T,       O [16 channels, 8 rows] = codes of V^T x w^T.
 // The order of the channels inside a K step, and of the positions inside a block of 16, is free, so both
-// operands are read from shared memory as they lie there.  Where the result must be good to fp32, or there
-// are at most four rows, the 8 columns are 4 rows in two fp16 parts each, which costs nothing then.
+// operands are read from shared memory as they lie there.  Where the result must be good to fp16 or
+// fp32, the 8 columns are fewer rows in two or three fp16 parts each.
 //
 // A CTA is four warps; warp w of part s of a (sequence, K/V head) takes the tiles of 32 positions
 // s * 4 + w, + 4 * splits, ...  Each warp streams its tiles' K and V rows (contiguous in a page) with
@@ -121,8 +121,9 @@ struct VCodes {
 //     core's sum (6e-5 of it), which is nothing in bf16.
 //   1 (fp16, or running sums kept): q' in parts of 11 bits on one fixed grid -- with the codes multiplied up to
 //     normal fp16 numbers every product and every sum of a part is exact -- so that a score has fp32's rounding and no
-//     other; the weights one fp16.
-//   2 (fp32): the same, V's codes multiplied up too and the weights in two fp16 parts.
+//     other; the weights in two fp16 parts, in columns that are there anyway (one: up to 4.1e-4 of an fp16 output, against
+//     2.3e-4 and the output's own rounding of 2.1e-4).
+//   2 (fp32): the same, V's codes multiplied up too, less the code nearest to the zero point.
 // The grid's unit hangs on the row's largest |q'|: two parts, 22 bits of that, do for fp16 outputs; fp32 ones and the
 // sums have three (a few large channels cost the others too much: 2e-5 of the output measured with two, 3e-7 with three).
 // Columns: RT = 1: row 0's part t in column 2t, the odd ones empty (a lane then has half the softmax to do);
@@ -134,7 +135,7 @@ struct DecShape {
     static constexpr int RB = D * BITS / 8;    // bytes of a packed row
     static constexpr uint32_t TILE = DEC_TILE * RB, STAGE = 2 * TILE;
     static constexpr size_t RING = (size_t)DEC_WARPS * DEC_STAGES * STAGE;
-    static constexpr size_t JOIN = (size_t)DEC_WARPS * ROWS * (D + 3) * 4;  // the warps' results, when they are joined
+    static constexpr size_t JOIN = (size_t)DEC_WARPS * ROWS * (D + 2) * 4;  // the warps' results, when they are joined
     static constexpr size_t SMEM = RING > JOIN ? RING : JOIN;
     static constexpr int PARTS = PREC == 0 ? 1 : RT <= 2 ? 3 : 2;  // of q'
     // row in the tile, and part, of column `col`
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
         return IN_RING ? reinterpret_cast<uint32_t *>(spare(i / FR)) + i % FR * 32 : s_qf + (nt * KP::N + i) * 32;
     };
     __shared__ __align__(16) uint8_t s_ref[S::RB];
-    __shared__ float s_fac[S::ROWS][32], s_max[S::ROWS], s_inv[S::ROWS], s_winv[S::ROWS];
+    __shared__ float s_fac[S::ROWS][32], s_max[S::ROWS], s_inv[S::ROWS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
     const Paged &p = a.p;
     const int split = blockIdx.x % a.splits;
@@ -325,16 +326,13 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
 
     float o[D / 16][NT][4];  // sums over the warp's positions: channels 2i, 2i + 1 of the lane's D / 8, two columns
     float m[NT][E], off[NT][E], l[NT][E];  // reference of the exponents, DEC_PSHIFT - m, sum
-    // Outputs are divided by the sum of the weights as rounded for their product, running sums by the weights' own
-    constexpr bool OWN = PREC == 1 && RT <= 2;
-    float lw[NT][E];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             m[nt][e] = -1e30f;
             off[nt][e] = vis[nt][e] > 0 ? 1e30f : -INFINITY;
-            l[nt][e] = lw[nt][e] = 0.f;
+            l[nt][e] = 0.f;
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
@@ -355,6 +353,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
     const int v0 = 2 * tq + (tq & 1), v1 = v0 ^ 1;
     const int part = S::part(2 * tq);  // of the lane's columns
     const bool head = part == 0;       // the lane's columns are the rows' first (or only) parts
+    const float second = part == 1 ? -1.f : 0.f;  // a weight's second part: less its first
     const float part_scale = part == 0 ? 1.f : part == 1 ? 0x1p-11f : part == 2 ? 0x1p-22f : 0.f;
 
     bool ok = true;
@@ -465,7 +464,6 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
                         m[nt][e] = mn;
                         off[nt][e] = (float)DEC_PSHIFT - mn;
                         l[nt][e] *= r;
-                        lw[nt][e] *= r;
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) {
                             o[c][nt][e] *= r;
@@ -492,18 +490,13 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
                     for (int e = 0; e < E; ++e) pv[e] = ex2(y[bk][nt][f][e]);
                     uint32_t hw = half2_bits(pv[0], pv[1]);
                     const float2 r2 = __half22float2(*reinterpret_cast<const __half2 *>(&hw));
-                    if (PREC == 2) {
+                    if (PREC) {  // two parts, in the columns of q's first two (what is in the others is not used)
 #pragma unroll
                         for (int e = 0; e < E; ++e) l[nt][e] += pv[e];
-                        const uint32_t lw = half2_bits(pv[0] - r2.x, pv[1] - r2.y);
-                        hw = part == 0 ? hw : part == 1 ? lw : 0u;
+                        hw = half2_bits(fmaf(r2.x, second, pv[0]), fmaf(r2.y, second, pv[1]));
                     } else {  // the rounded weights are summed: numerator and denominator hold the same ones
                         l[nt][0] += r2.x;
                         if (E == 2) l[nt][E - 1] += r2.y;
-                        if (OWN) {
-#pragma unroll
-                            for (int e = 0; e < E; ++e) lw[nt][e] += pv[e];
-                        }
                     }
                     w[nt][f] = mat_trans(hw);
                 }
@@ -546,14 +539,11 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
-            for (int f = 4; f < 32; f <<= 1) {
-                l[nt][e] += __shfl_xor_sync(FULL, l[nt][e], f);
-                if (OWN) lw[nt][e] += __shfl_xor_sync(FULL, lw[nt][e], f);
-            }
+            for (int f = 4; f < 32; f <<= 1) l[nt][e] += __shfl_xor_sync(FULL, l[nt][e], f);
     __syncthreads();  // every warp is done with its ring
     float *js = reinterpret_cast<float *>(smem);            // [warp][row][D]
     float *jm = js + DEC_WARPS * S::ROWS * D;               // [warp][row]
-    float *jl = jm + DEC_WARPS * S::ROWS, *jw = jl + DEC_WARPS * S::ROWS;
+    float *jl = jm + DEC_WARPS * S::ROWS;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -564,7 +554,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
                     float v = o[c][nt][2 * f + e];
-                    if (PREC == 2) v += __shfl_xor_sync(FULL, v, XOR);
+                    if (PREC) v += __shfl_xor_sync(FULL, v, XOR);
                     // the codes' power of two and the weights' 2^DEC_PSHIFT
                     v *= (float)(1 << ((PREC == 2 ? 10 : 24) - VC::pos(2 * c + f))) * (1.f / (float)(1 << DEC_PSHIFT));
                     if (head) js[(warp * S::ROWS + r) * D + gq * (D / 8) + 2 * c + f] = v;
@@ -572,7 +562,6 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
             if (gq == 0 && head) {
                 jm[warp * S::ROWS + r] = l[nt][e] == 0.f ? -INFINITY : m[nt][e];
                 jl[warp * S::ROWS + r] = l[nt][e] * (1.f / (float)(1 << DEC_PSHIFT));
-                jw[warp * S::ROWS + r] = (OWN ? lw[nt][e] : l[nt][e]) * (1.f / (float)(1 << DEC_PSHIFT));
             }
         }
     __syncthreads();
@@ -607,23 +596,15 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
     cluster.sync();
     for (int r = warp; r < rows; r += DEC_WARPS) {
         const float *om = cluster.map_shared_rank(jm, min(lane / DEC_WARPS, a.splits - 1));
-        const float *ol = om + (jl - jm), *ow = om + (jw - jm);
+        const float *ol = om + (jl - jm);
         const float mw = lane < all ? om[lane % DEC_WARPS * S::ROWS + r] : -INFINITY;
         float mt = mw;
         for (int f = 16; f > 0; f >>= 1) mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, f));
         const float f = mw == -INFINITY ? 0.f : ex2(mw - mt);
         float lt = lane < all ? ol[lane % DEC_WARPS * S::ROWS + r] * f : 0.f;
-        float wt = OWN && lane < all ? ow[lane % DEC_WARPS * S::ROWS + r] * f : 0.f;
-        for (int o = 16; o > 0; o >>= 1) {
-            lt += __shfl_xor_sync(FULL, lt, o);
-            if (OWN) wt += __shfl_xor_sync(FULL, wt, o);
-        }
+        for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(FULL, lt, o);
         s_fac[r][lane] = f;
-        if (lane == 0) {
-            s_max[r] = mt;
-            s_inv[r] = mt == -INFINITY ? 0.f : 1.f / lt;
-            s_winv[r] = mt == -INFINITY ? 0.f : 1.f / (OWN ? wt : lt);
-        }
+        if (lane == 0) s_max[r] = mt, s_inv[r] = mt == -INFINITY ? 0.f : 1.f / lt;
     }
     __syncthreads();
     for (int i = split * DEC_THREADS + tid; i < rows * D; i += a.splits * DEC_THREADS) {
@@ -655,7 +636,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
                 const int seen = L - n + r / a.G + 1;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (at[u] && pos[u] < seen) w[u] = fmaf(ex2(x[pos[u]] - s_max[r]), s_winv[r], w[u]);
+                    if (at[u] && pos[u] < seen) w[u] = fmaf(ex2(x[pos[u]] - s_max[r]), s_inv[r], w[u]);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
