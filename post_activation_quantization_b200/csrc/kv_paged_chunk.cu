@@ -9,9 +9,9 @@
 //   warp 12           issues the MMAs of both (warps 13-15 fill its warpgroup)
 // The two tiles share K and V and take turns on the tensor core: one's softmax runs while the other's
 // products do.  The codes come from global memory a tile ahead, are masked in place (kv_paged_attn.cuh) and
-// brought to small exact fp16 numbers by one fused multiply-add per two: K's relative to position 0's codes (a shift of all
-// scores of a row, which the softmax does not see; S then has the size of the scores' spread), V's relative to the code
-// nearest to the channel's zero point.
+// brought to small exact fp16 numbers by one fused multiply-add per two: K's relative to the first positions' mean (a shift
+// of all scores of a row, which the softmax does not see; S, and what the queries' rounding does to it, then have the size
+// of the scores' spread), V's relative to the code nearest to the channel's zero point.
 // Queries come from a first kernel as finished operand tiles, already scaled (q' = q s) and in the 128-byte swizzle.
 // Where the scores must be good to fp32 (fp32 queries, or running sums of weights), q' has two fp16 parts and S takes two
 // products.  fp32 outputs have W in two parts as well, tiles of 64 positions, and the products of a tile are added to O by
@@ -290,15 +290,33 @@ struct ChunkCodes {
     }
 };
 
-// Position 0's codes of quarter t, negated, as the K expansion subtracts them.
+// What is taken off K's codes of quarter t, negated: the mean of the first 16 positions' (of the last one's again where there
+// are fewer; all of one page), any choice being a shift of all scores of a row.  In sixteenths: exact in fp16.
 template <int BITS, int D>
-__device__ __forceinline__ void chunk_reference(const PagedAttnDev &a, int b, int h, int t, uint32_t (&ref)[KPairs<BITS, D>::N])
+__device__ __forceinline__ void chunk_reference(const PagedAttnDev &a, int b, int h, int t, int L, uint32_t (&ref)[KPairs<BITS, D>::N])
 {
+    constexpr int N = KPairs<BITS, D>::N, RB = D * BITS / 8;
     const Paged &p = a.p;
-    const int page = max(paged_page(p, b, 0), 0);
-    KPairs<BITS, D>::load(a.kq + paged_row(page, a.H, h, p.shift) * (D * BITS / 8), t, ref);
+    const uint8_t *rows = a.kq + paged_row(max(paged_page(p, b, 0), 0), a.H, h, p.shift) * RB;
+    constexpr int STEP = D == 128 ? 2 : 4;  // lanes of a quarter (chunk_share): every STEP-th; each reads STEP / 2 of the rows
+    const int r = (threadIdx.x & 31) / STEP;
+    uint32_t x[N];
+    KPairs<BITS, D>::load(rows + min(r, L - 1) * RB, t, x);
 #pragma unroll
-    for (int i = 0; i < KPairs<BITS, D>::N; ++i) ref[i] = code_up(ref[i]) ^ 0x80008000u;
+    for (int i = 0; i < N; ++i) ref[i] = code_up(x[i]);
+    if (STEP == 4) {
+        KPairs<BITS, D>::load(rows + min(r + 8, L - 1) * RB, t, x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) ref[i] = code_up_plus(x[i], ref[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __half2 v = *reinterpret_cast<const __half2 *>(&ref[i]);
+#pragma unroll
+        for (int o = STEP; o < 32; o <<= 1) v = __hadd2(v, __shfl_xor_sync(FULL, v, o));
+        v = __hmul2(v, __float2half2_rn(-1.f / 16.f));
+        ref[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
 }
 
 // ---- attention --------------------------------------------------------------------------------------------
@@ -308,7 +326,7 @@ struct ChunkShape {
     static constexpr int KEYS = PP == 2 ? 64 : 128;  // positions of a tile
     static constexpr uint32_t KV_SLAB = KEYS * 128, KV = SLABS * KV_SLAB;  // a K or V tile
     static constexpr uint32_t QT = QP * SLABS * CH_SLAB;                   // a query tile
-    static constexpr int STAGES = QP == 2 && PP == 1 && D == 128 ? 1 : 2;  // what 227 KB leave
+    static constexpr int STAGES = QP == 2 && PP == 1 && D == 128 ? 1 : 2;  // what 227 KB leave (a second one of K alone: no faster)
     static constexpr uint32_t SMEM = 1024 + 2 * QT + 2 * STAGES * KV;
     static constexpr uint32_t O_COL = 256;  // O of tile g at O_COL + g * D
 };
@@ -567,7 +585,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
         bool ok = true;
         if (j1 > j0) {
             uint32_t ref[KP::N], zc[KP::N];  // what is taken off K's and V's codes
-            chunk_reference<BITS, D>(a, b, h, t, ref);
+            chunk_reference<BITS, D>(a, b, h, t, L, ref);
 #pragma unroll
             for (int i = 0; i < KP::N; ++i)
                 zc[i] = half2_bits(code_offset(s_zc[t * (D / 4) + KP::code(i, 0)], KP::pos(i, 0)),
@@ -629,7 +647,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             }
             for (int i = 0; i < count && ok; ++i) {
                 const int st = i % ST, st1 = (i + 1) % ST;
-                if constexpr (PP == 2) {
+                if constexpr (PP == 2) {  // each product where it is added from; then both tiles' next scores
                     constexpr uint32_t pv64 = f16_idesc(CH_M, 64) | IDESC_B_MN;
                     for (int hf = 0; hf < HALVES && ok; ++hf)
                         for (int g = 0; g < nact && ok; ++g) {
@@ -656,28 +674,26 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                         scores(g, st1);
                         if (g == nact - 1) tc_commit(k_empty + 8 * st1);
                     }
-                    continue;
-                }
-                for (int g = 0; g < nact && ok; ++g) {
-                    const uint32_t tS = tmem + (uint32_t)g * CH_M, tO = tmem + S::O_COL + (uint32_t)g * D;
-                    if (!(ok = mbar_wait_bounded(p_full + 8 * g, i & 1, p.err))) break;
-                    if (g == 0 && !(ok = mbar_wait_bounded(v_full + 8 * st, (uint32_t)(i / ST) & 1, p.err))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int part = 0; part < PP; ++part)
+                } else {
+                    for (int g = 0; g < nact && ok; ++g) {
+                        const uint32_t tS = tmem + (uint32_t)g * CH_M, tO = tmem + S::O_COL + (uint32_t)g * D;
+                        if (!(ok = mbar_wait_bounded(p_full + 8 * g, i & 1, p.err))) break;
+                        if (g == 0 && !(ok = mbar_wait_bounded(v_full + 8 * st, (uint32_t)(i / ST) & 1, p.err))) break;
+                        tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < KEYS / 16; ++kk)
-                            tc_mma_f16_ts(tO, tS + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part,
-                                          sw128_mn_desc(sV + st * S::KV + kk * 2048, S::KV_SLAB), pv, i > 0 || (part | kk) != 0);
-                    tc_commit(o_done + 8 * g);
-                    if (g == nact - 1) tc_commit(v_empty + 8 * st);
-                    if (i + 1 == count) continue;
-                    if (g == 0 && !(ok = mbar_wait_bounded(k_full + 8 * st1, (uint32_t)((i + 1) / ST) & 1, p.err))) break;
-                    // S (and W in its place) is free once the products that read it are complete
-                    if (!(ok = mbar_wait_bounded(o_done + 8 * g, i & 1, p.err))) break;
-                    tc_fence_after();
-                    scores(g, st1);
-                    if (g == nact - 1) tc_commit(k_empty + 8 * st1);
+                            tc_mma_f16_ts(tO, tS + 32 * (kk >> 1) + 8 * (kk & 1),
+                                          sw128_mn_desc(sV + st * S::KV + kk * 2048, S::KV_SLAB), pv, i > 0 || kk != 0);
+                        tc_commit(o_done + 8 * g);
+                        if (g == nact - 1) tc_commit(v_empty + 8 * st);
+                        if (i + 1 == count) continue;
+                        if (g == 0 && !(ok = mbar_wait_bounded(k_full + 8 * st1, (uint32_t)((i + 1) / ST) & 1, p.err))) break;
+                        // S (and W in its place) is free once the products that read it are complete
+                        if (!(ok = mbar_wait_bounded(o_done + 8 * g, i & 1, p.err))) break;
+                        tc_fence_after();
+                        scores(g, st1);
+                        if (g == nact - 1) tc_commit(k_empty + 8 * st1);
+                    }
                 }
             }
             tc_commit(drain);  // tensor memory is released below: every issued product first
@@ -749,7 +765,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         int r0, t, ids[4];
         chunk_share<D>(tid & (CH_M - 1), r0, t);
         uint32_t ref[KP::N];
-        chunk_reference<BITS, D>(a, b, h, t, ref);
+        chunk_reference<BITS, D>(a, b, h, t, L, ref);
         ChunkCodes<BITS, D, CH_KEYS / 32> kc;
         chunk_pages(p, b, pos0, L, r0, ids);
         chunk_check(p, ids);
@@ -777,7 +793,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             if (i >= i1 || row >= R) return;
             const int tok = row / a.G, j = row - tok * a.G;
             const float2 st = *reinterpret_cast<const float2 *>(a.stat + 2 * ((int64_t)(s0 + tok) * a.Hq + h * a.G + j));
-            // scores are relative to position 0's, so the maximum is small enough for the sum's log to be added to it
+            // scores are relative to those of K's mean, so the maximum is small enough for the sum's log to be added to it
             f = make_float2(c.cx[(qslot + i) * CH_M + r], st.y > 0.f ? log2f(st.y) - st.x : st.y == 0.f ? -INFINITY : st.y);
             vis = L - n + tok + 1;
         };
