@@ -101,28 +101,31 @@ struct ChunkQ {
     }
 };
 
-// N consecutive elements (2 or 4, aligned to their size) of a tensor of run-time type
+// N consecutive elements (2 or 4, aligned to their size) of a tensor of run-time type, as they lie and as numbers
 template <int N>
-__device__ __forceinline__ void load_row(const void *p, int dtype, int64_t at, float (&v)[N])
+__device__ __forceinline__ void load_raw(const void *p, int dtype, int64_t at, uint32_t (&w)[N])
 {
     if (dtype == RPTQ_F32) {
 #pragma unroll
         for (int k = 0; k < N; k += 2) {
-            const float2 f = *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + at + k);
-            v[k] = f.x, v[k + 1] = f.y;
+            const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const float *>(p) + at + k);
+            w[k] = u.x, w[k + 1] = u.y;
         }
-        return;
-    }
-    uint32_t w[N / 2];
-    if constexpr (N == 4) {
+    } else if constexpr (N == 4) {
         const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at);
         w[0] = u.x, w[1] = u.y;
     } else {
         w[0] = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + at);
     }
+}
+template <int N>
+__device__ __forceinline__ void raw_floats(const uint32_t (&w)[N], int dtype, float (&v)[N])
+{
 #pragma unroll
     for (int k = 0; k < N / 2; ++k) {
-        if (dtype == RPTQ_F16) {
+        if (dtype == RPTQ_F32) {
+            v[2 * k] = __uint_as_float(w[2 * k]), v[2 * k + 1] = __uint_as_float(w[2 * k + 1]);
+        } else if (dtype == RPTQ_F16) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
             v[2 * k] = f.x, v[2 * k + 1] = f.y;
         } else {
@@ -158,6 +161,21 @@ __global__ void __launch_bounds__(CQ_THREADS)
     const int64_t i = slot - chunk_base(p, b, a.G, CH_M);
     const int64_t rows = (int64_t)n * a.G - i * CH_M;
     if (i < 0 || rows <= 0) return;
+    // Each warp's rows, U at a time, their loads together and a turn ahead.  (Loads of four rows at the turn's start: 52 us at
+    // 6144 rows of 32 heads against 34.)
+    constexpr int U = 4, W = CQ_THREADS / 32;
+    uint32_t raw[U][CPL];
+    auto fetch = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = (int)i * CH_M + r0 + u, tok = row / a.G, j = row - tok * a.G;
+            const int64_t at = (int64_t)(s0 + tok) * a.q_stride + (int64_t)(h * a.G + j) * D + lane * CPL;
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) raw[u][k] = 0;
+            if (r0 + u < rows) load_raw<CPL>(a.q, a.dtype, at, raw[u]);
+        }
+    };
+    fetch(warp * U);
     for (int d = tid; d < D; d += CQ_THREADS) {
         int col, pos;
         ChunkQ<BITS, D>::column(d, col, pos);
@@ -166,45 +184,36 @@ __global__ void __launch_bounds__(CQ_THREADS)
         s_down[d] = 1.f / (float)(1 << pos);
     }
     __syncthreads();
-    // four rows of a warp at a time, their loads together
-    constexpr int U = 4, W = CQ_THREADS / 32;
+    float sc[CPL], down[CPL];  // of the lane's channels
+    uint32_t to[CPL];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) sc[k] = s_s[lane * CPL + k], down[k] = s_down[lane * CPL + k], to[k] = s_at[lane * CPL + k];
     for (int r0 = warp * U; r0 < CH_M; r0 += W * U) {
         float v[U][CPL], m[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t row = i * CH_M + r0 + u;
-            const int tok = (int)(row / a.G), j = (int)(row - (int64_t)tok * a.G);
-            const int64_t at = (int64_t)(s0 + tok) * a.q_stride + (int64_t)(h * a.G + j) * D + lane * CPL;
-#pragma unroll
-            for (int k = 0; k < CPL; ++k) v[u][k] = 0.f;
-            if (r0 + u < rows) load_row<CPL>(a.q, a.dtype, at, v[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
+            raw_floats<CPL>(raw[u], a.dtype, v[u]);
             m[u] = 0.f;
 #pragma unroll
             for (int k = 0; k < CPL; ++k) {
-                v[u][k] *= s_s[lane * CPL + k];
+                v[u][k] *= sc[k];
                 m[u] = fmaxf(m[u], fabsf(v[u][k]));
             }
         }
+        if (r0 + W * U < CH_M) fetch(r0 + W * U);
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
             for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(FULL, m[u], o));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int r = r0 + u;
-            int ex = 0;
-            if (m[u] > 0.f && m[u] < INFINITY) frexpf(m[u], &ex);
-            ex = max(ex, -100);
+            const int ex = max((int)(__float_as_uint(m[u]) >> 23) - 126, -100);  // m in [2^(ex - 1), 2^ex)
             const float up = __uint_as_float((uint32_t)(127 + 15 - ex) << 23);  // 2^(15 - ex): 15 - ex <= 115
-            if (lane == 0) c.cx[((int64_t)h * c.slots + slot) * CH_M + r] = ldexpf(a.scale * LOG2E, ex - 15 + 10);
+            if (lane == 0) c.cx[((int64_t)h * c.slots + slot) * CH_M + r] = a.scale * LOG2E * __uint_as_float((uint32_t)(127 - 5 + ex) << 23);
 #pragma unroll
             for (int k = 0; k < CPL; ++k) {
-                const uint32_t sw = (s_at[lane * CPL + k] + r * 128) ^ ((r & 7) << 4);  // piece c of a row sits at c ^ (row mod 8)
-                const float down = s_down[lane * CPL + k];
-                float f = v[u][k] * up;
-                f *= down;
+                const uint32_t sw = (to[k] + r * 128) ^ ((r & 7) << 4);  // piece c of a row sits at c ^ (row mod 8)
+                const float f = v[u][k] * up * down[k];
                 const __half hi = __float2half_rn(f);
                 *reinterpret_cast<__half *>(tile + sw) = hi;
                 if (PARTS == 2) *reinterpret_cast<__half *>(tile + (D / 64) * CH_SLAB + sw) = __float2half_rn(f - __half2float(hi));
