@@ -18,9 +18,15 @@
 // the softmax's threads: the tensor core's own additions are cut off at the accumulator's last bit, and the many of a long
 // row would all err to the same side (4e-6 after 1287 positions, measured).
 //
+// Measured at 3 chunks of about 2048 tokens over about 6000 positions, 32 heads of 128, 3 bits, fp16: 495 us, 830 TFLOP/s (34
+// of them the queries' kernel), 0.50 of the tensor core's measured peak.  The exponentials (16 a clock and SM) take a third of
+// the time; what bounds it is the softmax's instructions as a whole, which run beside the other tile's products.
+//
 // Running sums: a third kernel goes over the positions again with the rows' maxima and sums known: tiles of 128
 // positions are the row operand, S^T = K q'^T, so that a thread owns a position and adds its weights in registers,
 // row tile by row tile, in a fixed order.
+// 2 chunks of 1024 tokens over about 8100 positions, 32 heads over 8, 4 bits, bf16: 563 us, some 5 % of it the
+// queries, 55 % the attention (1.7 waves of CTAs) and 40 % the sums.
 #include <algorithm>
 #include <type_traits>
 
