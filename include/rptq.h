@@ -409,9 +409,9 @@ int rptq_kv_paged_dequant(const uint8_t *pages, int H, int D, int bits, const in
  *   workspace    rptq_kv_paged_attention_workspace_size(...) bytes (0: may be NULL), 16-byte
  *                aligned; no initialisation, garbage afterwards.  Calls that may overlap need one each.
  * Sums, softmax statistics and outputs before their rounding to `dtype` are fp32.  For fp16 and
- * bf16 outputs the operands of the products carry 11 bits (a weight and, for bf16 or many rows, a
- * query times its scale, rounded to fp16: at most 2^-11 each); for fp32 outputs, and for the scores
- * behind running sums, 22 or more.  Results do not change from run to run.  A page id out of range is
+ * bf16 outputs the operands of the products (weights, queries times their scale) carry at least 11
+ * bits, as fp16 (at most 2^-11 off each); for fp32 outputs, and for the scores behind running sums, 22
+ * or more.  Results do not change from run to run.  A page id out of range is
  * read as page 0 (no weight is added there).
  * Fastest for D = 64 and 128, the head sizes of the tensor-core kernels; other D take a general one.
  */

@@ -14,9 +14,9 @@ Attention's bars follow from the arithmetic.  With q'_d = q_d s_d and the code k
     (2^-21, or 2^-10 for a numerator and a denominator of 11 bits) and, below the smallest part, by
     2^-24 of the row's largest weight;
   * sums over L positions take at most L/4 + 64 fp32 roundings, each counted 4 times;
-  * out_d = s_d (sum_p w_p k_pd - z_d), where a kernel may take the codes about their middle h = 2^(bits-1), as
-    s_d (sum_p w_p (k_pd - h) - (z_d - h)): the rounded sum is then up to sum_p w_p |k_pd - h| <= h whatever sum_p w_p k_pd
-    is (all codes 0: -h), so errors are relative to s_d (sum_p w_p k_pd + |z_d| + 2 h) = `mag`;
+  * out_d = s_d (sum_p w_p k_pd - z_d), where a kernel may take the codes about one of them, c <= 2 h - 1, h = 2^(bits-1), as
+    s_d (sum_p w_p (k_pd - c) - (z_d - c)): the rounded sum is then up to sum_p w_p |k_pd - c| < 2 h whatever sum_p w_p k_pd
+    is (all codes 0: -c), so errors are relative to s_d (sum_p w_p k_pd + |z_d| + 2 h) = `mag`;
   * the output is rounded to its type: half a step, eps/2, relative."""
 import math
 
@@ -212,6 +212,13 @@ ATTEND = [
     (2, 1, 96, 3, 16, [3, 40], [50, 41], "bf16", True),
     (1, 2, 32, 4, 32, [1, 70], [3, 100], "f32", False),
     (1, 1, 256, 3, 64, [2, 1], [90, 1], "f16", False),
+    (1, 2, 64, 4, 32, [20, 3], [700, 3], "f32", False),
+    (1, 1, 64, 3, 16, [300], [2100], "f32", True),
+    (1, 1, 128, 4, 64, [260, 9, 2], [1500, 9, 2], "f32", False),
+    (2, 4, 128, 4, 64, [2, 1], [900, 40], "f32", True),
+    (1, 8, 64, 3, 16, [1, 1], [640, 15], "f32", False),
+    (1, 1, 64, 4, 16, [9, 12], [9, 12], "f32", True),  # shorter than the 16 positions whose mean is taken off
+    (1, 2, 128, 3, 64, [8, 1], [2000, 3], "f16", False),
 ]
 
 
