@@ -531,7 +531,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             if (ok) {
                 constexpr float UNSHIFT = SHIFT == 0.f ? 1.f : 0x1p-5f;  // 2^-SHIFT
                 const float l = (lo2(l2) + hi2(l2)) * UNSHIFT;
-                const bool sees = l > 0.f || l != l;
+                // The reference has moved: the row saw a position of this part.  (The sum does not tell: a masked weight from
+                // exp2_poly is 2^-126, nothing beside a visible one but more than 0 without.)
+                const bool sees = m > -1e30f || l != l;
                 const int tok = row / a.G, jh = row - tok * a.G;
                 const int64_t orow = (int64_t)(s0 + tok) * a.Hq + h * a.G + jh;
                 const float inv = sees ? 1.f / l : 0.f;
