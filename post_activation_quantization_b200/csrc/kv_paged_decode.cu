@@ -306,7 +306,10 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < KP::N; ++i) qf[nt][i] = fragment(nt, i)[lane];
-    if (IN_RING) __syncthreads();  // read by all: the stages may be filled
+    if (IN_RING) {  // read by all: the stages may be filled, by copies that come after these stores and loads (another proxy's)
+        fence_proxy_async_smem();
+        __syncthreads();
+    }
 
     // Scores are taken relative to position 0's, subtracted in the (exact) sums of each part: what is left has the size
     // of the scores' spread, while q' code alone carries the channels' means times q.
@@ -531,7 +534,8 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
                     }
                 }
         }
-        __syncwarp();  // the stage has been read (its values went into the MMAs above)
+        fence_proxy_async_smem();
+        __syncwarp();  // the stage has been read (its values went into the MMAs above): the next turn's copy may fill it
     }
     if (!ok)  // a wait ran out: no copy may be in flight into this CTA's memory when it ends
         for (int i = max(0, issued - DEC_STAGES); i < issued; ++i)

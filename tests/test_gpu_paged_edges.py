@@ -1,6 +1,5 @@
 """Paged attention at its edges: rows that see nothing, and what surrounds them (against oracle/paged.py, with the bars of
 tests/test_gpu_paged.py)."""
-import numpy as np
 import pytest
 import torch
 
@@ -44,3 +43,22 @@ def test_rows_before_position_0_are_0_in_a_chunk(ns, lens, D, bits, dtype, sums)
     for b, (n, L) in enumerate(zip(ns, lens)):
         assert (out[c.start[b]:c.start[b] + max(0, n - L)] == 0).all()
     check_attention(c, q, out, dtype, weights=c.d["w"])
+
+
+@pytest.mark.parametrize("D,bits,page,dtype,sums", [(64, 4, 16, "f32", False), (128, 3, 64, "f16", False), (128, 4, 128, "bf16", False),
+                                                    (64, 3, 16, "bf16", True), (128, 3, 32, "f32", True)])
+def test_decode_rings_that_turn_many_times(D, bits, page, dtype, sums):
+    """One row to a K/V head: its query fragments lie in the last stage of every warp's ring until the first turn fills it.
+    Three to thirty turns a warp, the same result every time and the definition's."""
+    B = 80
+    c = Case(8, D, bits, page, [1] * B, [4000 - 47 * b for b in range(B)], seed=52, sums=sums)
+    q = c.queries(8, dtype)
+    qd = q.to(DEV)
+    first = c.attend(qd)
+    w1 = c.d["w"].clone() if sums else None
+    for _ in range(20):
+        if sums:
+            c.d["w"].copy_(torch.from_numpy(c.w0))
+        assert torch.equal(c.attend(qd), first)
+        assert not sums or torch.equal(c.d["w"], w1)
+    check_attention(c, q, first, dtype, weights=c.d["w"])
