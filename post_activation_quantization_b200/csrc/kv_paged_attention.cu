@@ -174,10 +174,11 @@ static cudaError_t launch_paged_attention_t(const PagedAttnArgs &a)
 {
     const Paged p{a.start, a.lens, a.table, a.B, a.max_pages, a.shift, a.n_pages, a.T, a.max_q, a.max_len, a.err};
     const T *q = static_cast<const T *>(a.q);
-    float *stat = a.weights ? static_cast<float *>(a.ws) : nullptr;
+    const bool sums = a.weights != nullptr && a.max_len > 0;
+    float *stat = sums ? static_cast<float *>(a.ws) : nullptr;
     paged_attention_general<T, BITS><<<(unsigned)(a.T * a.Hq), GA_THREADS, 0, a.stream>>>(
         q, a.q_stride, p, a.Hq, a.H, a.D, a.kq, a.vq, a.kt, a.scale, static_cast<T *>(a.out), stat);
-    if (a.weights)
+    if (sums)
         paged_weights_general<T, BITS>
             <<<(unsigned)((int64_t)((a.max_len + GA_WARPS - 1) / GA_WARPS) * a.B * a.H), GA_THREADS, 0, a.stream>>>(
                 q, a.q_stride, p, a.Hq, a.H, a.D, a.kq, a.kt, a.scale, stat, a.weights);
@@ -186,8 +187,10 @@ static cudaError_t launch_paged_attention_t(const PagedAttnArgs &a)
 
 cudaError_t launch_paged_attention(const PagedAttnArgs &a)
 {
-    if (paged_decode_takes(a.Hq, a.H, a.D, a.dtype, a.max_q, a.weights != nullptr)) return launch_paged_decode(a);
-    if (a.D == 64 || a.D == 128) return launch_paged_chunk(a);
+    if (a.max_len > 0) {  // else no position anywhere: rows of zeros, no sums, and a workspace of no bytes
+        if (paged_decode_takes(a.Hq, a.H, a.D, a.dtype, a.max_q, a.weights != nullptr)) return launch_paged_decode(a);
+        if (a.D == 64 || a.D == 128) return launch_paged_chunk(a);
+    }
     switch (a.dtype) {
     case RPTQ_F32: return a.bits == 4 ? launch_paged_attention_t<float, 4>(a) : launch_paged_attention_t<float, 3>(a);
     case RPTQ_F16: return a.bits == 4 ? launch_paged_attention_t<__half, 4>(a) : launch_paged_attention_t<__half, 3>(a);

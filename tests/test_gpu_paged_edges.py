@@ -62,3 +62,21 @@ def test_decode_rings_that_turn_many_times(D, bits, page, dtype, sums):
         assert torch.equal(c.attend(qd), first)
         assert not sums or torch.equal(c.d["w"], w1)
     check_attention(c, q, first, dtype, weights=c.d["w"])
+
+
+@pytest.mark.parametrize("ns", [[1, 1], [150, 3]])
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("dtype,sums", [("bf16", False), ("f16", True), ("f32", False), ("f32", True)])
+def test_no_position_anywhere(ns, D, dtype, sums):
+    """max_len = 0: every row is 0, no sum changes, no workspace is needed; a sequence that has positions all the same is out
+    of range."""
+    c = Case(2, D, 3, 16, ns, [0, 0], seed=53, rows_behind=2, sums=sums)
+    c.max_len = 0
+    assert rptq.rptq_kv_paged_attention_workspace_size(c.T, 4, 2, D, TD[dtype], 2, c.max_q, 0, sums) == 0
+    _, out = _attend_into_sevens(c, 4, dtype)
+    assert (out[:-2] == 0).all() and (out[-2:] == 7).all()
+    c.d["lens"][1] = 1
+    _, out = _attend_into_sevens(c, 4, dtype)
+    assert rptq.rptq_device_error() == rptq.RPTQ_DEVERR_RANGE
+    assert (out[:ns[0]] == 0).all() and (out[ns[0]:] == 7).all()
+    assert not sums or torch.equal(c.d["w"].cpu(), torch.from_numpy(c.w0))
