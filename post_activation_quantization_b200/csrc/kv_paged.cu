@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(EV_THREADS)
     if (h == 0 && rank == 0 && tid == 0) new_lens[b] = bad ? L : min(L, budget);
     if (bad || L <= budget) {  // the same in every CTA of the cluster
         const int n = bad ? 0 : L;
-        for (int j = rank * EV_THREADS + tid; j < budget; j += CS * EV_THREADS) list[j] = j < n ? j : -1;
+        for (int64_t j = rank * EV_THREADS + tid; j < budget; j += CS * EV_THREADS) list[j] = j < n ? (int)j : -1;
         return;
     }
     auto row_of = [&](int pos) -> int64_t { return paged_row(tab[pos >> p.shift], H, h, p.shift) + (pos & pmask); };

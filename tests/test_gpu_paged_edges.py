@@ -80,3 +80,14 @@ def test_no_position_anywhere(ns, D, dtype, sums):
     assert rptq.rptq_device_error() == rptq.RPTQ_DEVERR_RANGE
     assert (out[:ns[0]] == 0).all() and (out[ns[0]:] == 7).all()
     assert not sums or torch.equal(c.d["w"].cpu(), torch.from_numpy(c.w0))
+
+
+def test_eviction_with_the_largest_budget():
+    """A budget that no length reaches: the index of the list of kept positions goes up to 2^31 - 2."""
+    c = Case(1, 32, 4, 16, [0], [70], seed=54, sums=True)
+    d = c.d
+    new, kept = rptq.rptq_kv_paged_evict(d["k"], d["v"], d["w"], d["lens"], d["table"], 4, 2 ** 31 - 1, 5)
+    assert new.tolist() == [70] and kept.shape == (1, 1, 2 ** 31 - 1)
+    assert kept[0, 0, :70].tolist() == list(range(70))
+    assert all(bool((part == -1).all()) for part in kept[0, 0, 70:].split(1 << 28))
+    assert torch.equal(d["k"].cpu(), torch.from_numpy(c.k0)) and torch.equal(d["w"].cpu(), torch.from_numpy(c.w0))
