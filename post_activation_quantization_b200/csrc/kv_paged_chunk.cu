@@ -44,7 +44,7 @@ constexpr uint32_t CH_SLAB = CH_M * 128;  // 128 rows of 64 fp16
 // some y passes CH_YMAX); fp16's smallest step is then 2^-(24 + CH_PSHIFT) of a weight at the reference.  Outputs of 16 bits
 // take the largest score itself for m: its weight is a power of two and has no rounding.  fp32 outputs, whose weights have
 // two parts, take an integer: CH_PSHIFT - m and the factors are exact.  Running sums beside outputs of 16 bits need both, so
-// there the shift is 0 and y = x - m rounds once.
+// there y = x - m rounds once, and 2^y is multiplied by 2^CH_PSHIFT (exact).
 constexpr float CH_PSHIFT = 5.f, CH_YMAX = 15.f;
 
 // 2^y of two exponents on the FMA pipe: y = n + f with n the nearest integer (the sum with 1.5 * 2^23 holds it in its
@@ -353,7 +353,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     using S = ChunkShape<D, QP, PP>;
     using KP = KPairs<BITS, D>;
     constexpr int ST = S::STAGES, KEYS = S::KEYS;
-    constexpr float SHIFT = QP == 2 && PP == 1 ? 0.f : CH_PSHIFT;  // of the weights' exponents (see CH_PSHIFT)
+    // the weights' shift: in their exponents, or by a product behind them (see CH_PSHIFT)
+    constexpr bool AFTER = QP == 2 && PP == 1;
+    constexpr float SHIFT = AFTER ? 0.f : CH_PSHIFT, YMAX = AFTER ? CH_YMAX - CH_PSHIFT : CH_YMAX;
     constexpr int HALVES = D / 64;  // PP = 2: a tile's product, 64 channels at a time, lies beside S
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[4 * 2 + 4 * 2 + 2];
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                 // cx > 0, so the largest score is cx * the largest S
                 const float ytop = fmaf(top, cx, off);
                 float f = 1.f;
-                if (__any_sync(FULL, ytop > CH_YMAX)) {
+                if (__any_sync(FULL, ytop > YMAX)) {
                     if (live && ytop > SHIFT) {
                         const float mn = PP == 1 ? top * cx : ceilf(top * cx);
                         f = ex2(m - mn);
@@ -482,7 +484,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                     for (int k = 0; k < 16; ++k) {
                         const f32x2 y = fma2(mk2(__uint_as_float(v[q4][2 * k]), __uint_as_float(v[q4][2 * k + 1])), cx2, off2);
                         // (precise weights stay with the finer function)
-                        const f32x2 e = QP == 1 && k % CH_POLY == CH_POLY - 1 ? exp2_poly(y) : mk2(ex2(lo2(y)), ex2(hi2(y)));
+                        f32x2 e = QP == 1 && k % CH_POLY == CH_POLY - 1 ? exp2_poly(y) : mk2(ex2(lo2(y)), ex2(hi2(y)));
+                        if (AFTER) e = mul2(e, mk2(0x1p5f, 0x1p5f));
                         l2 = add2(l2, e);
                         w[k] = half2_bits(lo2(e), hi2(e));
                         if (PP == 2) {
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             ok = __all_sync(FULL, ok);
             tc_fence_after();
             if (ok) {
-                constexpr float UNSHIFT = SHIFT == 0.f ? 1.f : 0x1p-5f;  // 2^-SHIFT
+                constexpr float UNSHIFT = 0x1p-5f;  // 2^-CH_PSHIFT
                 const float l = (lo2(l2) + hi2(l2)) * UNSHIFT;
                 // The reference has moved: the row saw a position of this part.  (The sum does not tell: a masked weight from
                 // exp2_poly is 2^-126, nothing beside a visible one but more than 0 without.)

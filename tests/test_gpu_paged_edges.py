@@ -1,10 +1,12 @@
 """Paged attention at its edges: rows that see nothing, and what surrounds them (against oracle/paged.py, with the bars of
 tests/test_gpu_paged.py)."""
+import numpy as np
 import pytest
 import torch
 
+import oracle.paged as paged
 from post_activation_quantization_b200 import rptq
-from tests.gpu_common import DEV
+from tests.gpu_common import DEV, to_np
 from tests.test_gpu_paged import TD, Case, check_attention
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +93,34 @@ def test_eviction_with_the_largest_budget():
     assert kept[0, 0, :70].tolist() == list(range(70))
     assert all(bool((part == -1).all()) for part in kept[0, 0, 70:].split(1 << 28))
     assert torch.equal(d["k"].cpu(), torch.from_numpy(c.k0)) and torch.equal(d["w"].cpu(), torch.from_numpy(c.w0))
+
+
+@pytest.mark.parametrize("D,bits,n,dtype,sums", [
+    (64, 4, 40, "f16", True), (128, 3, 40, "bf16", True), (64, 3, 40, "f16", False), (128, 4, 40, "bf16", False), (128, 3, 40, "f32", True),
+    (64, 4, 1, "f16", True), (128, 3, 1, "f16", False), (128, 4, 1, "f32", False), (64, 3, 1, "bf16", False)])
+def test_one_position_above_a_long_tail(D, bits, n, dtype, sums):
+    """Position 0 (value 0) scores 25.5 binary orders above all others (the largest value): the output is the tail's alone.
+
+    A weight is held as fp16 times at least 2^4 where the largest is 1, so it is off by at most half of fp16's smallest
+    step: 2^-25 / 2^4 = 2^-29 of the largest, for each of the L - 1 positions of the tail (weights of 2^-25.5).  Beside that, of the
+    result: the output's rounding, eps / 2; 2^-11 for scores (q' is exact here; sums of D products of fp32's precision: 25.5 ln 2
+    (D/4 + 32) 2^-24 < 7e-5), exponentials (7.5e-5), codes as subnormals in the values' products (6e-5) and sums cut off
+    at 2^-23 in L / 16 steps (6e-5), together below 2^-11 = 4.9e-4; 2^-9 where the scores' codes are subnormals too (decode, bf16
+    without sums: 6e-5 of a score of 25.5 ln 2 = 17.7)."""
+    H, L, qmax, drop = 80, 2048, 2 ** bits - 1, 25.5  # (heads enough that the positions of a chunk are not split: one maximum for all)
+    c = Case(H, D, bits, 16, [n], [L], seed=55, sums=sums)
+    one = lambda s: (np.zeros(H * D, np.int32), np.array([s], np.float32), np.zeros(1, np.int32))  # noqa: E731
+    c.k_cal, c.v_cal = one(1.0), one(0.5)
+    c.k0[:], c.v0[:] = 0, 255  # all codes 0; all codes qmax
+    c.k0[c.table[0, 0], :, 0], c.v0[c.table[0, 0], :, 0] = 255, 0
+    for name, x in (("k", c.k0), ("v", c.v0)):
+        c.d[name].copy_(torch.from_numpy(x))
+    c.d["kc"], c.d["vc"] = ([torch.from_numpy(x).to(DEV) for x in cal] for cal in (c.k_cal, c.v_cal))
+    q = torch.full((n, H, D), drop * np.log(2.0) / (qmax * D ** 0.5), dtype=torch.float64).to(TD[dtype])
+    got = to_np(c.attend(q.to(DEV))).astype(np.float64)
+    ref = paged.attention(to_np(q).astype(np.float64), c.start, c.lens, c.table, c.k0, c.v0, c.k_cal, c.v_cal, bits)[0]
+    assert (ref > 0.5 * qmax * (L - 1) * 2.0 ** -25.7).all() and (ref < 0.5 * qmax * (L - 1) * 2.0 ** -25.3).all()
+    rel = 2.0 ** -11 + torch.finfo(TD[dtype]).eps / 2 + (2.0 ** -9 if dtype == "bf16" and n == 1 and not sums else 0.0)
+    err = np.abs(got - ref)
+    tol = 0.5 * qmax * (L - 1) * 2.0 ** -29 + rel * ref
+    assert (err <= tol).all(), f"worst error {err.max():.3e} of {ref.max():.3e}, over its bar {(err / tol).max():.3g}"
