@@ -40,12 +40,15 @@ constexpr int CH_SOFT_WARPS = 8, CH_PROD_WARPS = 4;
 constexpr int CH_PROD0 = CH_SOFT_WARPS, CH_MMA0 = CH_PROD0 + CH_PROD_WARPS;
 constexpr int CH_THREADS = 32 * (CH_MMA0 + 4);  // whole warpgroups: registers are moved between them
 constexpr uint32_t CH_SLAB = CH_M * 128;  // 128 rows of 64 fp16
-// Weights are held as 2^y, y = x - m + CH_PSHIFT for a reference m that follows the running maximum (it moves when
-// some y passes CH_YMAX); fp16's smallest step is then 2^-(24 + CH_PSHIFT) of a weight at the reference.  Outputs of 16 bits
-// take the largest score itself for m: its weight is a power of two and has no rounding.  fp32 outputs, whose weights have
-// two parts, take an integer: CH_PSHIFT - m and the factors are exact.  Running sums beside outputs of 16 bits need both, so
+// Weights are held as 2^y, y = x - m + shift for a reference m that follows the running maximum (it moves when some y passes
+// CH_YMAX); fp16's smallest step is then 2^-(24 + shift) of a weight at the reference, and a weight is off by half of that
+// at least.  Outputs of 16 bits take CH_PSHIFT, which lets the maximum grow by 2^10 before O is scaled again (2^-30 of the largest
+// weight for each position: 2^-13 over 131072), and the largest score itself for m: its weight is a power of two and has no
+// rounding.  fp32 outputs, whose weights have two parts and whose O is scaled at every tile in any case, take
+// CH_PSHIFT32, and an integer for m: shift - m and the factors are exact.  Running sums beside outputs of 16 bits need both, so
 // there y = x - m rounds once, and 2^y is multiplied by 2^CH_PSHIFT (exact).
-constexpr float CH_PSHIFT = 5.f, CH_YMAX = 15.f;
+constexpr int CH_PSHIFT = 5, CH_PSHIFT32 = 14;
+constexpr float CH_YMAX = 15.f;
 
 // 2^y of two exponents on the FMA pipe: y = n + f with n the nearest integer (the sum with 1.5 * 2^23 holds it in its
 // low bits), 2^f on [-1/2, 1/2] by the cubic of least relative error (7.5e-5, fitted for this; a weight's fp16 rounding
@@ -355,7 +358,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
     constexpr int ST = S::STAGES, KEYS = S::KEYS;
     // the weights' shift: in their exponents, or by a product behind them (see CH_PSHIFT)
     constexpr bool AFTER = QP == 2 && PP == 1;
-    constexpr float SHIFT = AFTER ? 0.f : CH_PSHIFT, YMAX = AFTER ? CH_YMAX - CH_PSHIFT : CH_YMAX;
+    constexpr int WSHIFT = PP == 2 ? CH_PSHIFT32 : CH_PSHIFT;
+    constexpr float SHIFT = AFTER ? 0.f : (float)WSHIFT, YMAX = AFTER ? CH_YMAX - WSHIFT : CH_YMAX;
     constexpr int HALVES = D / 64;  // PP = 2: a tile's product, 64 channels at a time, lies beside S
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[4 * 2 + 4 * 2 + 2];
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
                         const f32x2 y = fma2(mk2(__uint_as_float(v[q4][2 * k]), __uint_as_float(v[q4][2 * k + 1])), cx2, off2);
                         // (precise weights stay with the finer function)
                         f32x2 e = QP == 1 && k % CH_POLY == CH_POLY - 1 ? exp2_poly(y) : mk2(ex2(lo2(y)), ex2(hi2(y)));
-                        if (AFTER) e = mul2(e, mk2(0x1p5f, 0x1p5f));
+                        if (AFTER) e = mul2(e, mk2((float)(1 << WSHIFT), (float)(1 << WSHIFT)));
                         l2 = add2(l2, e);
                         w[k] = half2_bits(lo2(e), hi2(e));
                         if (PP == 2) {
@@ -532,7 +536,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1)
             ok = __all_sync(FULL, ok);
             tc_fence_after();
             if (ok) {
-                constexpr float UNSHIFT = 0x1p-5f;  // 2^-CH_PSHIFT
+                constexpr float UNSHIFT = 1.f / (float)(1 << WSHIFT);
                 const float l = (lo2(l2) + hi2(l2)) * UNSHIFT;
                 // The reference has moved: the row saw a position of this part.  (The sum does not tell: a masked weight from
                 // exp2_poly is 2^-126, nothing beside a visible one but more than 0 without.)

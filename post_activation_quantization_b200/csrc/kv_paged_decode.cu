@@ -33,9 +33,11 @@ constexpr int DEC_WARPS = 4, DEC_THREADS = 32 * DEC_WARPS;
 constexpr int DEC_TILE = 32;    // positions of a warp's tile: two blocks of 16
 constexpr int DEC_STAGES = 3;   // tiles of a warp's ring: two on the way while one is worked (four: fewer CTAs to an SM, slower)
 constexpr int DEC_CTAS_SM = 4;  // CTAs that share an SM: 128 registers a thread, 36 or 48 KB of rings
-// Weights are held as 2^y, y = x - m + DEC_PSHIFT for a reference m that follows the running maximum: y up to
-// DEC_YMAX fits fp16, and its smallest step is 2^-(24 + DEC_PSHIFT) of a weight at the reference.
-constexpr int DEC_PSHIFT = 5;
+// Weights are held as 2^y, y = x - m + shift for a reference m that follows the running maximum (an integer not below it when
+// it moves): y up to DEC_YMAX fits fp16, and its smallest step is 2^-(24 + shift) of a weight at the reference.  Outputs of
+// 16 bits leave the maximum room to grow before the sums are scaled again (a weight is off by 2^-29 of the largest at least: 2^-12
+// over 131072 positions); fp32 ones take the bits instead (2^-38).
+constexpr int DEC_PSHIFT = 5, DEC_PSHIFT32 = 14;
 constexpr float DEC_YMAX = 15.f;
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -156,6 +158,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
     using KP = KPairs<BITS, D>;
     using VC = VCodes<BITS, D>;
     constexpr int E = S::E;
+    constexpr int PSHIFT = PREC == 2 ? DEC_PSHIFT32 : DEC_PSHIFT;
     constexpr int XOR = RT <= 2 ? 1 : 2;  // lane distance of a row's first two parts
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[DEC_WARPS * DEC_STAGES];
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
     }
 
     float o[D / 16][NT][4];  // sums over the warp's positions: channels 2i, 2i + 1 of the lane's D / 8, two columns
-    float m[NT][E], off[NT][E], l[NT][E];  // reference of the exponents, DEC_PSHIFT - m, sum
+    float m[NT][E], off[NT][E], l[NT][E];  // reference of the exponents, PSHIFT - m, sum
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
                         }
                 }
         }
-        // exponents against the reference m: y = x - m + DEC_PSHIFT, -inf where the row does not see the position.
+        // exponents against the reference m: y = x - m + PSHIFT, -inf where the row does not see the position.
         // m only has to keep 2^y inside fp16; it moves when some y passes DEC_YMAX, seldom after the first tile.
         const bool whole = pos0 + DEC_TILE <= L - n + 1;  // every row sees the whole tile
         float y[2][NT][2][E];
@@ -466,10 +469,10 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
 #pragma unroll
                     for (int f = 4; f < 32; f <<= 1) mn = fmaxf(mn, __shfl_xor_sync(FULL, mn, f));
                     if (vis[nt][e] > 0 && mn > -1e30f) {
-                        mn = ceilf(mn);  // an integer: DEC_PSHIFT - m is exact, and so is the factor between two references
+                        mn = ceilf(mn);  // an integer: PSHIFT - m is exact, and so is the factor between two references
                         const float r = ex2(m[nt][e] - mn);
                         m[nt][e] = mn;
-                        off[nt][e] = (float)DEC_PSHIFT - mn;
+                        off[nt][e] = (float)PSHIFT - mn;
                         l[nt][e] *= r;
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) {
@@ -563,13 +566,13 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
                 for (int f = 0; f < 2; ++f) {
                     float v = o[c][nt][2 * f + e];
                     if (PREC) v += __shfl_xor_sync(FULL, v, XOR);
-                    // the codes' power of two and the weights' 2^DEC_PSHIFT
-                    v *= (float)(1 << ((PREC == 2 ? 10 : 24) - VC::pos(2 * c + f))) * (1.f / (float)(1 << DEC_PSHIFT));
+                    // the codes' power of two and the weights' 2^PSHIFT
+                    v *= (float)(1 << ((PREC == 2 ? 10 : 24) - VC::pos(2 * c + f))) * (1.f / (float)(1 << PSHIFT));
                     if (head) js[(warp * S::ROWS + r) * D + gq * (D / 8) + 2 * c + f] = v;
                 }
             if (gq == 0 && head) {
                 jm[warp * S::ROWS + r] = l[nt][e] == 0.f ? -INFINITY : m[nt][e];
-                jl[warp * S::ROWS + r] = l[nt][e] * (1.f / (float)(1 << DEC_PSHIFT));
+                jl[warp * S::ROWS + r] = l[nt][e] * (1.f / (float)(1 << PSHIFT));
             }
         }
     __syncthreads();

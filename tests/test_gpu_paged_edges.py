@@ -95,19 +95,10 @@ def test_eviction_with_the_largest_budget():
     assert torch.equal(d["k"].cpu(), torch.from_numpy(c.k0)) and torch.equal(d["w"].cpu(), torch.from_numpy(c.w0))
 
 
-@pytest.mark.parametrize("D,bits,n,dtype,sums", [
-    (64, 4, 40, "f16", True), (128, 3, 40, "bf16", True), (64, 3, 40, "f16", False), (128, 4, 40, "bf16", False), (128, 3, 40, "f32", True),
-    (64, 4, 1, "f16", True), (128, 3, 1, "f16", False), (128, 4, 1, "f32", False), (64, 3, 1, "bf16", False)])
-def test_one_position_above_a_long_tail(D, bits, n, dtype, sums):
-    """Position 0 (value 0) scores 25.5 binary orders above all others (the largest value): the output is the tail's alone.
-
-    A weight is held as fp16 times at least 2^4 where the largest is 1, so it is off by at most half of fp16's smallest
-    step: 2^-25 / 2^4 = 2^-29 of the largest, for each of the L - 1 positions of the tail (weights of 2^-25.5).  Beside that, of the
-    result: the output's rounding, eps / 2; 2^-11 for scores (q' is exact here; sums of D products of fp32's precision: 25.5 ln 2
-    (D/4 + 32) 2^-24 < 7e-5), exponentials (7.5e-5), codes as subnormals in the values' products (6e-5) and sums cut off
-    at 2^-23 in L / 16 steps (6e-5), together below 2^-11 = 4.9e-4; 2^-9 where the scores' codes are subnormals too (decode, bf16
-    without sums: 6e-5 of a score of 25.5 ln 2 = 17.7)."""
-    H, L, qmax, drop = 80, 2048, 2 ** bits - 1, 25.5  # (heads enough that the positions of a chunk are not split: one maximum for all)
+def _above_a_tail(D, bits, n, dtype, sums, drop=25.5):
+    """(output, its 64-bit value, tail's value times its positions): position 0 (value 0) scores `drop` binary orders above all
+    others, whose value is the largest there is, so that the output is the tail's alone."""
+    H, L, qmax = 80, 2048, 2 ** bits - 1  # (heads enough that the positions of a chunk are not split: one maximum for all)
     c = Case(H, D, bits, 16, [n], [L], seed=55, sums=sums)
     one = lambda s: (np.zeros(H * D, np.int32), np.array([s], np.float32), np.zeros(1, np.int32))  # noqa: E731
     c.k_cal, c.v_cal = one(1.0), one(0.5)
@@ -119,8 +110,31 @@ def test_one_position_above_a_long_tail(D, bits, n, dtype, sums):
     q = torch.full((n, H, D), drop * np.log(2.0) / (qmax * D ** 0.5), dtype=torch.float64).to(TD[dtype])
     got = to_np(c.attend(q.to(DEV))).astype(np.float64)
     ref = paged.attention(to_np(q).astype(np.float64), c.start, c.lens, c.table, c.k0, c.v0, c.k_cal, c.v_cal, bits)[0]
-    assert (ref > 0.5 * qmax * (L - 1) * 2.0 ** -25.7).all() and (ref < 0.5 * qmax * (L - 1) * 2.0 ** -25.3).all()
+    unit = 0.5 * qmax * (L - 1)
+    assert (ref > unit * 2.0 ** -(drop + 0.2)).all() and (ref < unit * 2.0 ** -(drop - 0.2)).all()
+    return got, ref, unit
+
+
+@pytest.mark.parametrize("D,bits,n,dtype,sums", [
+    (64, 4, 40, "f16", True), (128, 3, 40, "bf16", True), (64, 3, 40, "f16", False), (128, 4, 40, "bf16", False),
+    (64, 4, 1, "f16", True), (128, 3, 1, "f16", False), (64, 3, 1, "bf16", False)])
+def test_one_position_above_a_long_tail(D, bits, n, dtype, sums):
+    """A weight is held as fp16 times at least 2^4 where the largest is 1, so it is off by at most half of fp16's smallest
+    step: 2^-25 / 2^4 = 2^-29 of the largest, for each of the L - 1 positions of the tail (weights of 2^-25.5).  Beside that, of the
+    result: the output's rounding, eps / 2; 2^-11 for scores (q' is exact here; sums of D products of fp32's precision: 25.5 ln 2
+    (D/4 + 32) 2^-24 < 7e-5), exponentials (7.5e-5), codes as subnormals in the values' products (6e-5) and sums cut off
+    at 2^-23 in L / 16 steps (2e-5), together below 2^-11 = 4.9e-4; 2^-9 where the scores' codes are subnormals too (decode, bf16
+    without sums: 6e-5 of a score of 25.5 ln 2 = 17.7)."""
+    got, ref, unit = _above_a_tail(D, bits, n, dtype, sums)
     rel = 2.0 ** -11 + torch.finfo(TD[dtype]).eps / 2 + (2.0 ** -9 if dtype == "bf16" and n == 1 and not sums else 0.0)
-    err = np.abs(got - ref)
-    tol = 0.5 * qmax * (L - 1) * 2.0 ** -29 + rel * ref
+    err, tol = np.abs(got - ref), unit * 2.0 ** -29 + rel * ref
+    assert (err <= tol).all(), f"worst error {err.max():.3e} of {ref.max():.3e}, over its bar {(err / tol).max():.3g}"
+
+
+@pytest.mark.parametrize("D,bits,n,sums", [(64, 3, 40, False), (128, 4, 40, True), (64, 4, 1, False), (128, 3, 1, True), (64, 4, 3, False)])
+def test_one_position_above_a_long_tail_in_fp32(D, bits, n, sums):
+    """Two fp16 parts times at least 2^13: half of the smallest step is 2^-25 / 2^13 = 2^-38 of the largest weight.  Of the result:
+    scores 25.5 ln 2 (D/4 + 32) 2^-24 < 7e-5 and 17.7 2^-22 for q' in 22 bits, exponents below 64 rounded to 2^-19, the rest less: 1e-4."""
+    got, ref, unit = _above_a_tail(D, bits, n, "f32", sums)
+    err, tol = np.abs(got - ref), unit * 2.0 ** -38 + 1e-4 * ref
     assert (err <= tol).all(), f"worst error {err.max():.3e} of {ref.max():.3e}, over its bar {(err / tol).max():.3g}"
