@@ -214,7 +214,8 @@ PyObject *dequant(PyObject *, PyObject *const *v, Py_ssize_t n)
     const at::Tensor *given = a.tensor();
     const int code = a.narrow();
     const Pool p(a, t[0], t[1], bits);
-    a.ok = a.ok && (given ? given->dim() == 3 && dtype_code(given->scalar_type()) >= 0 : T >= 0 && code >= 0 && code <= 2);
+    a.ok = a.ok && (given ? given->dim() == 3 && dtype_code(given->scalar_type()) >= 0 && (T < 0 || T == given->size(0))
+                          : T >= 0 && code >= 0 && code <= 2);
     if (!a.ok) return status_and(RPTQ_ERR_INVALID_ARG, at::Tensor());
     const Stream stream(a, v[11]);
     at::Tensor out = given ? *given

@@ -425,7 +425,7 @@ def rptq_kv_paged_append(k_new, v_new, start, lens, page_table, k_pages, v_pages
 def rptq_kv_paged_dequant(pages, page_table, start, begin, cluster, scale, zero, bits: int, T: int | None = None, out=None,
                           out_dtype=torch.float32, stream=None):
     """Positions begin[b] + i of sequence b read back into row start[b] + i of [T, H, D].  T: the rows
-    (a host value; without it, out's)."""
+    (a host value; without it, out's; another number than out's is refused)."""
     st, out = (_marshal or _paged()).dequant(pages, page_table, start, begin, cluster, scale, zero, bits, -1 if T is None else T,
                                              out, _DT.get(out_dtype, -1), _handle(stream))
     if st:

@@ -138,3 +138,15 @@ def test_one_position_above_a_long_tail_in_fp32(D, bits, n, sums):
     got, ref, unit = _above_a_tail(D, bits, n, "f32", sums)
     err, tol = np.abs(got - ref), unit * 2.0 ** -38 + 1e-4 * ref
     assert (err <= tol).all(), f"worst error {err.max():.3e} of {ref.max():.3e}, over its bar {(err / tol).max():.3g}"
+
+
+def test_read_back_refuses_rows_that_are_not_outs():
+    c = Case(2, 64, 3, 16, [3], [20], seed=56)
+    args = lambda **k: rptq.rptq_kv_paged_dequant(c.d["k"], c.d["table"], c.d["start"], c.d["lens"] * 0, *c.d["kc"], 3, **k)  # noqa: E731
+    want = args(T=3)
+    out = torch.empty_like(want)
+    assert args(out=out) is out and torch.equal(out, want)
+    assert args(T=3, out=out) is out and torch.equal(out, want)
+    for T in (0, 2, 4):
+        with pytest.raises(rptq.RptqError):
+            args(T=T, out=out)
