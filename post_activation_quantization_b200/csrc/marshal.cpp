@@ -75,7 +75,7 @@ struct Args {
     {
         if (t == nullptr) return nullptr;
         ok &= t->scalar_type() == type && t->is_cuda() && t->get_device() == dev && t->sizes() == shape &&
-              (t->numel() == 0 || (t->stride(2) == 1 && t->stride(1) == shape[2]));
+              (t->numel() == 0 || (t->stride(2) == 1 && (shape[1] == 1 || t->stride(1) == shape[2])));
         return ok ? t->data_ptr() : nullptr;
     }
 };

@@ -150,3 +150,18 @@ def test_read_back_refuses_rows_that_are_not_outs():
     for T in (0, 2, 4):
         with pytest.raises(rptq.RptqError):
             args(T=T, out=out)
+
+
+def test_rows_of_one_head_may_have_any_head_stride():
+    """[T, 1, D] as a transposed [1, T, D]: dense rows, whatever the stride of the one head."""
+    c = Case(1, 64, 3, 16, [3], [20], seed=57)
+    d, x = c.d, c.tokens(c.mk, "f16").to(DEV)
+    odd = x.reshape(1, 3, 64).transpose(0, 1)
+    assert odd.shape == (3, 1, 64) and odd.stride(1) != 64
+    pools = []
+    for k in (x, odd):
+        pool = d["k"].clone()
+        rptq.rptq_kv_paged_append(k, None, d["start"], d["lens"], d["table"], pool, None, *d["kc"], None, None, None, 3)
+        pools.append(pool)
+    assert torch.equal(*pools)
+    assert torch.equal(c.attend(odd), c.attend(x))
