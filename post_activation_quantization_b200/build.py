@@ -17,7 +17,6 @@ LIB = os.path.join(PKG, "librptq.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "calib.cu", "kmeans.cu", "ln_quant.cu", "kv_quant.cu", "dequant.cu", "kv_attention.cu", "explicit_reorder.cu", "linear.cu",
            "kv_paged.cu", "kv_paged_attention.cu", "kv_paged_decode.cu", "kv_paged_chunk.cu"]
-MARSHAL = os.path.join(PKG, "_marshal.so")  # argument marshalling of the paged-cache calls (host code only)
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -41,10 +40,16 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def marshal_path() -> str:
+    """The binding's file, named by what it was compiled against: one of another Python or PyTorch is never loaded."""
+    import torch
+    return os.path.join(PKG, f"_marshal-{sys.implementation.cache_tag}-torch{torch.__version__}.so")
+
+
 def build_marshal(force: bool = False) -> str:
-    src = os.path.join(CSRC, "marshal.cpp")
-    if not force and not _stale(MARSHAL, [src, os.path.join(ROOT, "include", "rptq.h")]):
-        return MARSHAL
+    out, src = marshal_path(), os.path.join(CSRC, "marshal.cpp")
+    if not force and not _stale(out, [src, os.path.join(ROOT, "include", "rptq.h")]):
+        return out
     import sysconfig
 
     import torch
@@ -52,12 +57,17 @@ def build_marshal(force: bool = False) -> str:
     inc = [f for d in (os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
                        os.path.join(cuda, "include"), sysconfig.get_paths()["include"]) for f in ("-isystem", d)]
     lib = os.path.join(home, "lib")
-    tmp = MARSHAL + f".tmp{os.getpid()}"
-    subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-                           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, src, "-o", tmp,
-                           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"])
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+    tmp = out + f".tmp{os.getpid()}"
+    try:
+        subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+                               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, src, "-o", tmp,
+                               "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"])
+    except Exception:
+        if os.path.exists(out):
+            os.remove(out)  # an older source's: not to be loaded in its place
+        raise
+    os.replace(tmp, out)
+    return out
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, jobs: int = 8) -> str:

@@ -392,7 +392,9 @@ def _paged():
     global _marshal
     if _marshal is None:
         import importlib.util
-        path = os.path.join(_PKG, "_marshal.so")
+
+        from . import build
+        path = build.marshal_path()
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with `python -m post_activation_quantization_b200.build`")
         spec = importlib.util.spec_from_file_location("_marshal", path)
