@@ -1,4 +1,4 @@
-"""The build's two products: the library, and the paged-cache calls' binding, made for one Python and PyTorch."""
+"""The build's two products: the library, and the paged-cache calls' binding, which only those calls need."""
 import os
 import subprocess
 import sys
@@ -11,6 +11,12 @@ from post_activation_quantization_b200 import build
 
 def _fail(*a, **k):
     raise subprocess.CalledProcessError(1, "g++")
+
+
+def test_library_is_built_where_the_binding_cannot_be(monkeypatch, capsys):
+    monkeypatch.setattr(build, "build_marshal", _fail)
+    assert build.build() == build.LIB and os.path.exists(build.LIB)
+    assert "no binding" in capsys.readouterr().err
 
 
 def test_binding_belongs_to_this_python_and_torch(monkeypatch):
