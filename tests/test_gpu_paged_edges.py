@@ -6,6 +6,7 @@ import torch
 
 import oracle.paged as paged
 from post_activation_quantization_b200 import rptq
+from tests import paged_bars
 from tests.gpu_common import DEV, to_np
 from tests.test_gpu_paged import TD, Case, check_attention
 
@@ -165,3 +166,15 @@ def test_rows_of_one_head_may_have_any_head_stride():
         pools.append(pool)
     assert torch.equal(*pools)
     assert torch.equal(c.attend(odd), c.attend(x))
+
+
+@pytest.mark.parametrize("seed", [71, 72])
+@pytest.mark.parametrize("case", paged_bars.CASES, ids=str)
+def test_attention_of_16_bits_in_norm(case, seed):
+    """Every 16-bit kernel within a bar that a mask off by one position does not pass."""
+    H, G, D, bits, page, ns, lens, dtype, sums = case
+    c = Case(H, D, bits, page, ns, lens, seed=seed, sums=sums)
+    q = paged_bars.queries(c, G, dtype)
+    got = to_np(c.attend(q.to(DEV))).astype(np.float64)
+    err, bar = paged_bars.check_norm(c, to_np(q).astype(np.float64), got, dtype)
+    print(f"error {err:.2e} bar {bar:.2e}")
