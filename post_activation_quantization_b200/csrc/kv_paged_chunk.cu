@@ -41,8 +41,8 @@ constexpr int CH_PROD0 = CH_SOFT_WARPS, CH_MMA0 = CH_PROD0 + CH_PROD_WARPS;
 constexpr int CH_THREADS = 32 * (CH_MMA0 + 4);  // whole warpgroups: registers are moved between them
 constexpr uint32_t CH_SLAB = CH_M * 128;  // 128 rows of 64 fp16
 // Weights are held as 2^y, y = x - m + shift for a reference m that follows the running maximum (it moves when some y passes
-// CH_YMAX); fp16's smallest step is then 2^-(24 + shift) of a weight at the reference, and a weight is off by half of that
-// at least.  Outputs of 16 bits take CH_PSHIFT, which lets the maximum grow by 2^10 before O is scaled again (2^-30 of the largest
+// CH_YMAX); fp16's smallest step is then 2^-(24 + shift) of a weight at the reference, and a weight, however small, may be off
+// by half of that.  Outputs of 16 bits take CH_PSHIFT, which lets the maximum grow by 2^10 before O is scaled again (2^-30 of the largest
 // weight for each position: 2^-13 over 131072), and the largest score itself for m: its weight is a power of two and has no
 // rounding.  fp32 outputs, whose weights have two parts and whose O is scaled at every tile in any case, take
 // CH_PSHIFT32, and an integer for m: shift - m and the factors are exact.  Running sums beside outputs of 16 bits need both, so

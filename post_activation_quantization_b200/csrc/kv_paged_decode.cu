@@ -34,11 +34,12 @@ constexpr int DEC_TILE = 32;    // positions of a warp's tile: two blocks of 16
 constexpr int DEC_STAGES = 3;   // tiles of a warp's ring: two on the way while one is worked (four: fewer CTAs to an SM, slower)
 constexpr int DEC_CTAS_SM = 4;  // CTAs that share an SM: 128 registers a thread, 36 or 48 KB of rings
 // Weights are held as 2^y, y = x - m + shift for a reference m that follows the running maximum (an integer not below it when
-// it moves): y up to DEC_YMAX fits fp16, and its smallest step is 2^-(24 + shift) of a weight at the reference.  Outputs of
-// 16 bits leave the maximum room to grow before the sums are scaled again (a weight is off by 2^-29 of the largest at least: 2^-12
-// over 131072 positions); fp32 ones take the bits instead (2^-38).
-constexpr int DEC_PSHIFT = 5, DEC_PSHIFT32 = 14;
-constexpr float DEC_YMAX = 15.f;
+// it moves, which is when some y passes YMAX): 2^YMAX fits fp16, and its smallest step is 2^-(24 + shift) of a weight at the
+// reference.  Outputs of 16 bits leave the maximum room to grow before the sums are scaled again (however small, a weight
+// may be off by 2^-29 of the largest: 2^-12 over 131072 positions); fp32 ones give up room for bits: 2^-36, 2^-19 over 131072.  (8 sequences
+// of 8000 positions, 32 heads over 8 of 128 / 64 over 8 of 64: shift 5 42.2 / 47.6 us, 10 42.4 / 48.2, 12 43.0 / 50.5, 14 45.4 / 57.8.)
+constexpr int DEC_PSHIFT = 5, DEC_PSHIFT32 = 12;
+constexpr float DEC_YMAX = 15.f, DEC_YMAX32 = 15.9f;
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1)
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
     using VC = VCodes<BITS, D>;
     constexpr int E = S::E;
     constexpr int PSHIFT = PREC == 2 ? DEC_PSHIFT32 : DEC_PSHIFT;
+    constexpr float YMAX = PREC == 2 ? DEC_YMAX32 : DEC_YMAX;
     constexpr int XOR = RT <= 2 ? 1 : 2;  // lane distance of a row's first two parts
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[DEC_WARPS * DEC_STAGES];
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
                 }
         }
         // exponents against the reference m: y = x - m + PSHIFT, -inf where the row does not see the position.
-        // m only has to keep 2^y inside fp16; it moves when some y passes DEC_YMAX, seldom after the first tile.
+        // m only has to keep 2^y inside fp16; it moves when some y passes YMAX, seldom after the first tile.
         const bool whole = pos0 + DEC_TILE <= L - n + 1;  // every row sees the whole tile
         float y[2][NT][2][E];
         auto hide = [&]() {
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? (PREC == 2 ? 3 : DEC_CT
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < E; ++e) top = max3f(top, y[bk][nt][0][e], y[bk][nt][1][e]);
-        if (__any_sync(FULL, top > DEC_YMAX)) {
+        if (__any_sync(FULL, top > YMAX)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
