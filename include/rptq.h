@@ -408,11 +408,16 @@ int rptq_kv_paged_dequant(const uint8_t *pages, int H, int D, int bits, const in
  *   weights      NULL, or the running sums to add to.
  *   workspace    rptq_kv_paged_attention_workspace_size(...) bytes (0: may be NULL), 16-byte
  *                aligned; no initialisation, garbage afterwards.  Calls that may overlap need one each.
- * Sums, softmax statistics and outputs before their rounding to `dtype` are fp32.  For fp16 and
- * bf16 outputs the operands of the products (weights, queries times their scale) carry at least 11
- * bits, as fp16 (at most 2^-11 off each); for fp32 outputs, and for the scores behind running sums, 22
- * or more.  Results do not change from run to run.  A page id out of range is
- * read as page 0 (no weight is added there).
+ * Sums, softmax statistics and outputs before their rounding to `dtype` are fp32.  The operands of
+ * the products are fp16 numbers or sums of some.  D = 64 and 128, at most off by, whichever is more:
+ *                          queries times their scale          weights
+ *     fp16, bf16 outputs   2^-11, 2^-22 of the row's largest  2^-11, 2^-29 of the row's largest
+ *     fp32 outputs         2^-22, 2^-31 of the row's largest  2^-22, 2^-36 of the row's largest
+ * (a cubic with a relative error of 7.5e-5 serves some exponentials of 16-bit outputs).  The queries
+ * behind running sums are held as for fp32 outputs, the sums' own weights are fp32 numbers.  Other D:
+ * fp32 throughout.
+ * Results do not change from run to run.  A page id out of range is read as page 0 (no weight is
+ * added there).  `out` must not overlap q, nor the workspace anything else.
  * Fastest for D = 64 and 128, the head sizes of the tensor-core kernels; other D take a general one.
  */
 size_t rptq_kv_paged_attention_workspace_size(int64_t T, int Hq, int H, int D, int dtype, int B,

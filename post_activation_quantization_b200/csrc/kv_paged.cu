@@ -20,8 +20,9 @@ namespace rptq {
 // A thread owns 8 consecutive channels, whose coefficients stay in registers, and walks the rows of
 // its CTA's chunk of the batch; blockIdx.y is the slab of blockDim.x * 8 channels, blockIdx.z the
 // tensor.  Where each row of the chunk lives is looked up once per CTA.  Both directions move each
-// byte once and are bound by HBM at large batches and by the launch at small ones (9 prompts of about 1100 tokens, 96 heads of 128,
-// 3 bits: append and read-back 206 us, 5.0 TB/s; 8 x 2048 positions read back, K and V: 174 us, 5.0 TB/s).
+// byte once and are bound by HBM at large batches and by the launch at small ones (calls one behind another, each on other inputs:
+// 9 prompts of about 1100 tokens, 96 heads of 128, 3 bits: append and read-back 219 us, 4.7 TB/s; 8 x 2048 positions read back,
+// K and V: 179 us, 4.85 TB/s).
 constexpr int PG_THREADS = 256;
 constexpr int PG_ROWS = 256;  // most rows of a CTA's chunk
 constexpr int PG_UNROLL = 4;  // 16-byte loads (words, for the read-back) of a step, the next step's issued before it
@@ -307,8 +308,8 @@ cudaError_t launch_paged_dequant(const PagedDequantArgs &a)
 // list moves from position kept[j] >= j to j: a batch of rows is loaded by the whole cluster, then stored.  A row
 // stored at j < i is never one that a later entry i reads (kept[i] >= i), so the only hazard is inside a batch, and one
 // cluster barrier between its loads and stores covers it.  The bound is the latency of those steps, so few (sequence, head)
-// pairs get a wide cluster.  (With the read-back of what is left: 16 x 32 heads of about 2048 to 1024, 3 bits, 108 us; 8 heads of
-// 32700 to 4096, 4 bits, 36 us.)
+// pairs get a wide cluster.  (16 x 32 heads of about 2048 to 1024, 3 bits: 61 us, with the read-back of what is left 108; 8 heads
+// of 32700 to 4096, 4 bits: 30 and 36 us.)
 constexpr int EV_SMALL = 256;  // threads of a CTA where there are many
 constexpr int EV_UNITS = 4;   // units of a batch per thread
 constexpr int EV_LOADS = 8;   // weights of a thread in flight together

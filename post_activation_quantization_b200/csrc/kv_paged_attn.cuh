@@ -6,12 +6,10 @@
 // and one mask leaves a code, or one code in each half of a 32-bit word, as a matrix operand.  The power
 // of two is taken out of the other operand (queries) or of the result (outputs).
 //     x_p = scale sum_d q_d s_d (code_pd - z_d):  the z part is the same for every position of a row and
-//           drops out of the softmax;  q'_d = q_d s_d goes in as fp16, scaled by a power of two per row
-//           that puts its largest |q'| in [2^14, 2^15);
+//           drops out of the softmax;  q'_d = q_d s_d goes in scaled by a power of two per row;
 //     out_d = s_d (sum_p w_p (code_pd - c_d) / sum_p w_p - (z_d - c_d)),  c_d = 0, or the code nearest to z_d.
-// Where the result must be good to fp32 (fp32 queries; running sums of weights, which are fp32 and
-// long-lived) an operand is split into two fp16 parts, 22 bits together; elsewhere q' and w carry fp16's
-// 11 bits (an error of 2^-11 at most, below the output's own rounding to bf16 or fp16).
+// Where more than fp16's 11 bits of an operand are needed (fp32 outputs; the scores behind running sums, which are fp32
+// and long-lived) it goes in as several fp16 parts; how many, and on which grid, each kernel says for itself.
 #pragma once
 
 #include "kv_paged.cuh"

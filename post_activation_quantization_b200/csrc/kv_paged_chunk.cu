@@ -18,15 +18,16 @@
 // the softmax's threads: the tensor core's own additions are cut off at the accumulator's last bit, and the many of a long
 // row would all err to the same side (4e-6 after 1287 positions, measured).
 //
-// Measured at 3 chunks of about 2048 tokens over about 6000 positions, 32 heads of 128, 3 bits, fp16: 495 us, 830 TFLOP/s (34
-// of them the queries' kernel), 0.50 of the tensor core's measured peak.  The exponentials (16 a clock and SM) take a third of
-// the time; what bounds it is the softmax's instructions as a whole, which run beside the other tile's products.
+// Measured (calls one behind another, each on other inputs) at 3 chunks of about 2048 tokens over about 6000 positions, 32 heads
+// of 128, 3 bits, fp16: 503 us (34 of them the queries' kernel), 820 TFLOP/s, 0.50 of the tensor core's measured peak.  No
+// unit is full (tensor core 0.46, special functions 0.40, issue slots 0.44): a tile's W V begins when all its weights are
+// there, and its next scores when W V is done, so that the two tiles in turn leave both idle about half of the time.
 //
 // Running sums: a third kernel goes over the positions again with the rows' maxima and sums known: tiles of 128
 // positions are the row operand, S^T = K q'^T, so that a thread owns a position and adds its weights in registers,
 // row tile by row tile, in a fixed order.
-// 2 chunks of 1024 tokens over about 8100 positions, 32 heads over 8, 4 bits, bf16: 563 us, some 5 % of it the
-// queries, 55 % the attention (1.7 waves of CTAs) and 40 % the sums.
+// 2 chunks of 1024 tokens over about 8100 positions, 32 heads over 8, 4 bits, bf16: 600 us (each kernel by itself: queries 19,
+// attention 345 in 1.7 waves of CTAs, sums 258).
 #include <algorithm>
 #include <type_traits>
 
@@ -52,7 +53,7 @@ constexpr float CH_YMAX = 15.f;
 
 // 2^y of two exponents on the FMA pipe: y = n + f with n the nearest integer (the sum with 1.5 * 2^23 holds it in its
 // low bits), 2^f on [-1/2, 1/2] by the cubic of least relative error (7.5e-5, fitted for this; a weight's fp16 rounding
-// is up to 4.9e-4), n added to the exponent.  y below -126 counts as -126.  The special-function unit gives 16 results a clock
+// is up to 4.9e-4), n added to the exponent.  y below -126 counts as -126, a masked one too: its weight is not 0 but 2^-126.  The special-function unit gives 16 results a clock
 // and SM, which the tensor core's two products of a tile take no longer than: one weight in CH_POLY comes from here.
 __device__ __forceinline__ f32x2 exp2_poly(f32x2 y)
 {
@@ -145,7 +146,7 @@ __device__ __forceinline__ void raw_floats(const uint32_t (&w)[N], int dtype, fl
 
 // ---- the queries as operand tiles -----------------------------------------------------------------------
 // One CTA per (tile slot, head), a warp to a row.  PARTS = 1: fp16 of q' scaled so that the row's largest is in
-// [2^14, 2^15); 2: and what that rounding leaves, as fp16 too: 22 bits of every element.  (Two integers on one grid
+// [2^14, 2^15); 2: and what that rounding leaves, as fp16 too: 22 bits of every element, or 2^-31 of the row's largest.  (Two integers on one grid
 // relative to the row's largest would keep the sums of the first part exact, but a row with an outlier then leaves its
 // other channels few bits: 3.6e-6 of the running sums instead of 2e-8, measured.)
 constexpr int CQ_THREADS = 256;

@@ -16,9 +16,10 @@
 // memory, write the outputs, and add to the running sums, each for the positions whose scores it kept.  More parts (long
 // contexts, few heads) are joined by a second kernel.
 //
-// Measured: 16 sequences of 2048 positions, 32 heads of 128, 3 bits, fp16: 40.5 us, 2.5 TB/s of codes; 8 of about 2047, 96 heads,
-// with sums: 60 us; 2 of about 131000, 32 heads over 8, 4 bits: 64 us, 4.1 TB/s.  What bounds it is the issue of the masks and
-// matrix instructions of each code, not HBM (6.6 TB/s).
+// Measured (calls one behind another, each on other inputs): 16 sequences of 2048 positions, 32 heads of 128, 3 bits, fp16: 43 us,
+// 2.4 TB/s of codes; 8 of about 2047, 96 heads, with sums: 61.5 us; 2 of about 131000, 32 heads over 8, 4 bits: 67.6 us,
+// 3.85 TB/s.  No unit is full (first case: issue slots 0.52, ALU 0.52, matrix pipe 0.22, HBM 0.36 of 6.6 TB/s): a warp works a
+// tile as one chain of dependent steps, and the 12 to 16 warps of an SM do not cover its latency.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -124,12 +125,12 @@ struct VCodes {
 };
 
 // RT rows to a column tile of 8.  PREC says what the result must be good to:
-//   0 (bf16): q' one fp16, the codes as they are.  A product with a subnormal keeps 10 bits less in the tensor
+//   0 (bf16): q' and the weights one fp16, the codes as they are.  A product with a subnormal keeps 10 bits less in the tensor
 //     core's sum (6e-5 of it), which is nothing in bf16.
 //   1 (fp16, or running sums kept): q' in parts of 11 bits on one fixed grid -- with the codes multiplied up to
 //     normal fp16 numbers every product and every sum of a part is exact -- so that a score has fp32's rounding and no
 //     other; the weights in two fp16 parts, in columns that are there anyway (one: up to 4.1e-4 of an fp16 output, against
-//     2.3e-4 and the output's own rounding of 2.1e-4).
+//     1.5e-4 to 3.1e-4, most of it the output's own rounding).  V's codes stay subnormals (6e-5).
 //   2 (fp32): the same, V's codes multiplied up too, less the code nearest to the zero point.
 // The grid's unit hangs on the row's largest |q'|: two parts, 22 bits of that, do for fp16 outputs; fp32 ones and the
 // sums have three (a few large channels cost the others too much: 2e-5 of the output measured with two, 3e-7 with three).
