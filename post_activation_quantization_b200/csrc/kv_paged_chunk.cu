@@ -13,8 +13,9 @@
 // of all scores of a row, which the softmax does not see; S, and what the queries' rounding does to it, then have the size
 // of the scores' spread), V's relative to the code nearest to the channel's zero point.
 // Queries come from a first kernel as finished operand tiles, already scaled (q' = q s) and in the 128-byte swizzle.
-// For outputs of 16 bits W is one fp16, and without sums q' is too: 2^-11 at most of each, either way, which adds 2e-5 to 1e-4
-// to the 2e-4 of an fp16 output's own rounding; the rows' sums take the weights before that rounding, in fp32.
+// For outputs of 16 bits W is one fp16, and without sums q' is too: 2^-11 at most of each, either way, which takes
+// an fp16 output's error from 2.1e-4, its own rounding, to 2.1e-4 to 2.7e-4; the rows' sums take the weights before that
+// rounding, in fp32.
 // Where the scores must be good to fp32 (fp32 queries, or running sums of weights), q' has two fp16 parts and S takes two
 // products.  fp32 outputs have W in two parts as well, tiles of 64 positions, and the products of a tile are added to O by
 // the softmax's threads: the tensor core's own additions are cut off at the accumulator's last bit, and the many of a long
